@@ -47,9 +47,9 @@
  *     decoded weights and activations that stay finite in float32.
  *   - Fault injection, for tests of error propagation: with the environment
  *     variable MOE_MXFP4_FAULT set to a launch site (router, route, sort,
- *     quant, gateup, down, combine, dflash; the fused path's one launch of
- *     both projections is the gateup and the down site), a call that
- *     reaches that site returns MOE_ERR_HIP there without launching, as a
+ *     quant, gateup, down, combine, dflash, plan, rope, kvread, attn;
+ *     the fused path's one launch of both projections is the gateup and
+ *     the down site), a call that reaches that site returns MOE_ERR_HIP there without launching, as a
  *     failed launch would;
  *     the kernels queued before it stay queued.  Read on every call.
  *   - Logging: with MOE_MXFP4_LOG set (to anything but "0") when a context
@@ -403,6 +403,227 @@ moe_status moe_mxfp4_dflash_accept(int32_t batch, int32_t block, int32_t vocab,
                                    const float* r, int32_t* n_accepted,
                                    int32_t* next_token, void* workspace,
                                    size_t workspace_bytes, void* hip_stream);
+
+/*
+ * The attention half of a verify step: a paged key/value cache, the plan of
+ * its pages, the norms and rotation of queries and keys that also write the
+ * cache, and attention over it.  The pages verify drafted blocks of up to 8
+ * tokens with the target model and draft them with a sliding-window drafter
+ * that fills a masked block in one pass (techllm.github.io "Xiaomi MiMo x
+ * TileRT", section "2. DFlash"); they give no cache, layout or API.  None of
+ * these calls is context-bound, and every one can be captured into a graph.
+ *
+ * THE CACHE holds num_pages pages of page_size tokens for kv_heads heads of
+ * head_dim = D elements.  A slot is page * page_size + row.  Keys and values
+ * are arrays of pages, each page an array of heads:
+ *   MOE_KV_BF16   k, v: bf16 [page][head][row][D]; no scales.
+ *   MOE_KV_MXFP4  E2M1 codes and one E8M0 byte per 32 elements of a row, as in
+ *                 the weights above (element 2c in the low nibble of byte c).
+ *     k        uint8 [page][head][row][D/2]
+ *     k_scale  uint8 [page][head][row][D/32]
+ *     v        uint8 [page][head][row/n][16][row%n][D/32], n = 512/D: byte c
+ *              of a row is stored at piece c / (D/32), so that 16 bytes hold
+ *              the same D/16 elements of n consecutive rows: what a lane of
+ *              the matrix-core operand reads along the keys
+ *     v_scale  uint8 [page][head][row/8][D/32][row%8]
+ * Each of k and v has num_pages * kv_heads * page_size * D * 2 bytes (bf16) or
+ * D/2 (MXFP4) per row, each scale array D/32 per row (moe_mxfp4_kv_cache_bytes).
+ * Limits: head_dim 64 or 128, page_size 16, 32, 64, 128 or 256, num_pages * page_size below
+ * 2^31, kv_heads 1..1024.  Device buffers are 16-byte aligned and caller-owned.
+ */
+typedef enum { MOE_KV_BF16 = 0, MOE_KV_MXFP4 = 1 } moe_kv_format;
+
+typedef struct {
+    uint32_t struct_size;    /* sizeof(moe_mxfp4_kv_cache)                      */
+    int32_t format;          /* moe_kv_format                                   */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    void* k;
+    void* v;
+    uint8_t* k_scale;        /* NULL for MOE_KV_BF16                            */
+    uint8_t* v_scale;        /* NULL for MOE_KV_BF16                            */
+} moe_mxfp4_kv_cache;
+
+/* Bytes of each of k and v, and of each scale array (0 for bf16), of a cache
+ * of this format and these sizes (the pointers are not looked at).  Errors:
+ * INVALID_ARG, UNSUPPORTED_SHAPE. */
+moe_status moe_mxfp4_kv_cache_bytes(const moe_mxfp4_kv_cache* cache, size_t* data_bytes, size_t* scale_bytes);
+
+/*
+ * Cache plan: block tables and slot maps on the device, from request lengths,
+ * without a host synchronisation.  Request b has ctx_lens[b] tokens in the
+ * cache and brings new_lens[b] more (their rows are packed request after
+ * request); new_lens[b] = -1: the request has ended and gives its pages back.
+ * All arrays are device int32:
+ *   block_table [B][max_blocks]  in and out: entries 0 .. held[b]-1 are the
+ *               request's pages; new pages are appended, other entries stay
+ *   held        [B]   pages each request holds (kept from the previous call:
+ *               a request whose ctx shrank after a rejection keeps its pages)
+ *   free_ring   [num_pages]  in and out: free pages, first taken first
+ *   free_state  [2]   position of the first free page in the ring, and count
+ *   held_out [B], free_state_out [2]   the same after the call; must not be
+ *               the input arrays (a caller keeps two of each and swaps them)
+ *   cu_q        [B+1] first row of each request, min(sum of max(new, 0), num_tokens)
+ *   kv_lens     [B]   ctx + new; 0 for refused and ended requests
+ *   slots, positions [num_tokens]  cache slot and position of every row; -1
+ *               for rows of refused requests and rows behind the last request
+ *   refused     [1]   number of refused requests
+ * A request is refused when ctx < 0, new < -1, ctx + new > max_blocks *
+ * page_size, its rows do not end within num_tokens, held is outside
+ * 0..max_blocks, or it needs pages and the pages needed up to and including it
+ * (over the requests with none of these faults, in order) exceed the free
+ * count.  A refused request keeps its pages and gets none; its rows keep their
+ * place.  An ended request whose held is outside 0..max_blocks, or whose pages would
+ * overfill the ring, is refused as well.  A free_state outside the ring (first
+ * outside 0..num_pages-1 or count outside 0..num_pages) offers and takes no page.  A
+ * table entry outside the cache gives slot -1.  The result does not depend on
+ * timing, and repeating the call on the same inputs repeats it.
+ * Limits: 0 <= batch <= 4096, num_tokens >= 0, max_blocks >= 1, page_size as
+ * above, num_pages >= 1, num_tokens <= 2^30, num_pages * page_size and
+ * max_blocks * page_size below 2^31.  batch = 0 still writes cu_q[0], slots, positions, refused and
+ * free_state_out.
+ * Errors: INVALID_ARG (null pointer, sizes, an output that is its input),
+ * UNSUPPORTED_SHAPE, ALIGNMENT, HIP.
+ */
+typedef struct {
+    uint32_t struct_size;    /* sizeof(moe_mxfp4_plan_args)                     */
+    int32_t batch;
+    int32_t num_tokens;
+    int32_t max_blocks;
+    int32_t page_size;
+    int32_t num_pages;
+    const int32_t* ctx_lens;
+    const int32_t* new_lens;
+    int32_t* block_table;
+    const int32_t* held;
+    int32_t* held_out;
+    int32_t* free_ring;
+    const int32_t* free_state;
+    int32_t* free_state_out;
+    int32_t* cu_q;
+    int32_t* kv_lens;
+    int32_t* slots;
+    int32_t* positions;
+    int32_t* refused;
+} moe_mxfp4_plan_args;
+moe_status moe_mxfp4_cache_plan(const moe_mxfp4_plan_args* args, void* hip_stream);
+
+/*
+ * Norms of queries and keys for each head, the position rotation, and the
+ * cache write, in one launch.  For every token t with positions[t] >= 0 (the
+ * others are left alone: no output row of theirs is touched):
+ *   y = x * rsqrt(mean(x^2) + eps) * weight for every head x of q and k, in
+ *   float32 (weight bf16 [D]; a NULL weight leaves that operand unnormalised);
+ *   the first rot_dim elements of y are rotated in pairs (a, b) ->
+ *   (a cos - b sin, b cos + a sin) by the angle positions[t] * inv_freq[i],
+ *   formed in 64 bits (inv_freq double [rot_dim/2]); pair i is elements
+ *   (i, i + rot_dim/2), or (2i, 2i + 1) with interleaved != 0.
+ *   q_out, k_out: bf16 [T][heads][D], [T][kv_heads][D].  With a cache, the
+ *   rotated key and v go to slots[t]: rounded to bf16, or quantised from
+ *   float32 to MXFP4 by the rule of moe_mxfp4_quantize_weights (a block with
+ *   an infinite or NaN element gets the scale byte 0xFF, NaN); a slot outside the
+ *   cache writes nothing there.  Slots of one call must differ.
+ * q, k, v: bf16, token t at t * stride elements, heads at D elements, so they
+ * may be parts of one projection's output.  q_out may be q, and k_out k, where
+ * their strides are heads * D and kv_heads * D; otherwise nothing may overlap.
+ * cache NULL: no write; v, v_stride and slots are then ignored and k_out is needed.
+ * With a cache k_out may be NULL.
+ * Limits: head_dim 64 or 128 (and the cache's), rot_dim 0..head_dim in steps
+ * of 16, heads, kv_heads 1..1024, strides multiples of 8 and at least heads * D
+ * (kv_heads * D), eps finite and >= 0, T below 2^24.  T = 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, HIP.
+ */
+typedef struct {
+    uint32_t struct_size;    /* sizeof(moe_mxfp4_rope_args)                     */
+    int32_t num_tokens;
+    int32_t heads;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t rot_dim;
+    int32_t interleaved;
+    float eps;
+    int64_t q_stride;
+    int64_t k_stride;
+    int64_t v_stride;
+    const void* q;
+    const void* k;
+    const void* v;
+    const void* q_weight;    /* bf16 [D] or NULL                                */
+    const void* k_weight;
+    const double* inv_freq;  /* [rot_dim/2]; NULL only for rot_dim 0            */
+    const int32_t* positions;
+    const int32_t* slots;
+    void* q_out;
+    void* k_out;
+} moe_mxfp4_rope_args;
+moe_status moe_mxfp4_qk_norm_rope(const moe_mxfp4_rope_args* args, const moe_mxfp4_kv_cache* cache,
+                                  void* hip_stream);
+
+/*
+ * The values that a cache holds at n slots (device int32 [n]): k, v (device)
+ * bf16 [n][kv_heads][D]; either may be NULL.  E2M1 values times their scale
+ * are exact in bf16 below its overflow; a scale byte 0xFF reads as NaN.  A slot outside the cache reads
+ * as zeros.  n * kv_heads below 2^28.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * ALIGNMENT, HIP.
+ */
+moe_status moe_mxfp4_kv_read(const moe_mxfp4_kv_cache* cache, const int32_t* slots, int32_t n, void* k, void* v,
+                             void* hip_stream);
+
+/*
+ * Attention over the cache for packed rows of B sequences: single tokens,
+ * drafted blocks and prompts alike.  Sequence b has the query rows cu_q[b] ..
+ * cu_q[b+1]-1 and kv_lens[b] tokens in the cache, its own rows' among them; row
+ * i of its n is at position p = kv_lens[b] - n + i.  Key j < kv_lens[b] is visible to
+ * it when j <= p (causal != 0) or always (causal = 0, the rows see each other
+ * whole), and, with window > 0, when p - j < window or j < sinks.  Query head
+ * h reads key/value head h / (heads / kv_heads).
+ *   out = sum_j softmax_j(scale * q.k_j) v_j over the visible keys
+ * A row that sees no key (a refused request, p < 0) gives zeros.  What is not
+ * visible has no influence, infinities and NaN in the cache included; keys in
+ * pages outside the cache are not visible.  Scores, softmax statistics and sums are
+ * float32; softmax weights enter the second product as bf16.  Rows outside
+ * every sequence are left as they were.  The result does not depend on timing.
+ *   q, out   bf16, token t at t * stride elements, heads at D elements; out
+ *            must not overlap q
+ *   block_table int32 [B][max_blocks], cu_q int32 [B+1], kv_lens int32 [B]
+ * cu_q ascends; it is clamped to 0..num_tokens and kv_lens to 0..max_blocks * page_size.
+ * max_q and max_kv are the longest n and kv_lens the caller expects: they
+ * shape the launch; sequences beyond them are still computed in full, slower.
+ * workspace: moe_mxfp4_attention_workspace_bytes (may be 0; then NULL is
+ * fine), no initial contents needed; calls that overlap in time need distinct
+ * workspaces.
+ * Limits: head_dim 64 or 128, heads a multiple of kv_heads and at most 16384,
+ * num_tokens * heads below 2^30, batch * kv_heads at most 2^20, max_q, max_kv >= 1, window, sinks >= 0, sinks
+ * only with a window, scale finite and > 0, strides multiples of 8 and at
+ * least heads * D, batch 0..65535.  batch = 0 or num_tokens = 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, ALIGNMENT, WORKSPACE, HIP.
+ */
+typedef struct {
+    uint32_t struct_size;    /* sizeof(moe_mxfp4_attn_args)                     */
+    int32_t batch;
+    int32_t num_tokens;
+    int32_t heads;
+    int32_t max_q;
+    int32_t max_kv;
+    int32_t max_blocks;
+    int32_t causal;
+    int32_t window;          /* 0: none                                         */
+    int32_t sinks;
+    float scale;
+    int64_t q_stride;
+    int64_t out_stride;
+    const void* q;
+    void* out;
+    const int32_t* block_table;
+    const int32_t* cu_q;
+    const int32_t* kv_lens;
+} moe_mxfp4_attn_args;
+/* 0 for arguments that moe_mxfp4_attention refuses (pointers are not looked at). */
+size_t moe_mxfp4_attention_workspace_bytes(const moe_mxfp4_attn_args* args, const moe_mxfp4_kv_cache* cache);
+moe_status moe_mxfp4_attention(const moe_mxfp4_attn_args* args, const moe_mxfp4_kv_cache* cache, void* workspace,
+                               size_t workspace_bytes, void* hip_stream);
 
 /*
  * Measurement probes, for reading roofline fractions against what this GPU

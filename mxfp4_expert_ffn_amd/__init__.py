@@ -9,9 +9,13 @@ Names follow the C ABI: ``MoeMxfp4`` wraps ``moe_mxfp4_create / _forward /
 _destroy / _workspace_bytes / _debug_dequant``; ``quantize_weights`` wraps
 ``moe_mxfp4_quantize_weights``; ``dflash_accept`` wraps
 ``moe_mxfp4_dflash_accept`` (the rejection-sampling pass of a verify step).
+The attention half of the step: ``KvCache`` (a paged cache's buffers),
+``cache_plan``, ``qk_norm_rope``, ``attention`` and ``kv_read`` wrap the
+entries of the same names.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -24,6 +28,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED_S
                 6: "MOE_ERR_HIP", 7: "MOE_ERR_INTERNAL"}
 ACT_BF16, ACT_MXFP8_E4M3 = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
+KV_BF16, KV_MXFP4 = 0, 1
 
 # Every symbol include/moe_mxfp4.h declares.
 EXPORTS = ("moe_mxfp4_status_string", "moe_mxfp4_abi_version", "moe_mxfp4_create",
@@ -32,7 +37,9 @@ EXPORTS = ("moe_mxfp4_status_string", "moe_mxfp4_abi_version", "moe_mxfp4_create
            "moe_mxfp4_stage_times", "moe_mxfp4_tiled_scale_bytes", "moe_mxfp4_tile_weights",
            "moe_mxfp4_quantize_act_mxfp8", "moe_mxfp4_router_logits", "moe_mxfp4_forward_hidden",
            "moe_mxfp4_dflash_workspace_bytes", "moe_mxfp4_dflash_accept", "moe_mxfp4_probe",
-           "moe_mxfp4_forward_noalloc", "moe_mxfp4_device_status", "moe_mxfp4_debug_hidden")
+           "moe_mxfp4_forward_noalloc", "moe_mxfp4_device_status", "moe_mxfp4_debug_hidden",
+           "moe_mxfp4_kv_cache_bytes", "moe_mxfp4_cache_plan", "moe_mxfp4_qk_norm_rope", "moe_mxfp4_kv_read",
+           "moe_mxfp4_attention_workspace_bytes", "moe_mxfp4_attention")
 # Scratch bytes moe_mxfp4_forward_noalloc holds per GPU (MOE_MXFP4_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 64 << 20
 # Largest batch (tokens x top_k) the fused path runs (MOE_MXFP4_FUSED_MAX_PAIRS);
@@ -63,6 +70,37 @@ class Weights(ctypes.Structure):
 class Routing(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("topk_ids", "topk_w", "expert_offsets",
                                                "sorted_pairs")]
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = ([("struct_size", ctypes.c_uint32)] +
+                [(n, ctypes.c_int32) for n in ("format", "num_pages", "page_size", "kv_heads", "head_dim")] +
+                [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")])
+
+
+class PlanArgs(ctypes.Structure):
+    _fields_ = ([("struct_size", ctypes.c_uint32)] +
+                [(n, ctypes.c_int32) for n in ("batch", "num_tokens", "max_blocks", "page_size", "num_pages")] +
+                [(n, ctypes.c_void_p) for n in ("ctx_lens", "new_lens", "block_table", "held", "held_out", "free_ring",
+                                                "free_state", "free_state_out", "cu_q", "kv_lens", "slots",
+                                                "positions", "refused")])
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = ([("struct_size", ctypes.c_uint32)] +
+                [(n, ctypes.c_int32) for n in ("num_tokens", "heads", "kv_heads", "head_dim", "rot_dim",
+                                               "interleaved")] + [("eps", ctypes.c_float)] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")] +
+                [(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_weight", "k_weight", "inv_freq", "positions",
+                                                "slots", "q_out", "k_out")])
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = ([("struct_size", ctypes.c_uint32)] +
+                [(n, ctypes.c_int32) for n in ("batch", "num_tokens", "heads", "max_q", "max_kv", "max_blocks",
+                                               "causal", "window", "sinks")] + [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "out_stride")] +
+                [(n, ctypes.c_void_p) for n in ("q", "out", "block_table", "cu_q", "kv_lens")])
 
 
 _lib = None
@@ -114,6 +152,18 @@ def lib():
         L.moe_mxfp4_dflash_workspace_bytes.restype = sz
         L.moe_mxfp4_dflash_accept.argtypes = [i32, i32, i32, P, P, P, P, P, P, P, P, sz, P]
         L.moe_mxfp4_dflash_accept.restype = ctypes.c_int
+        L.moe_mxfp4_kv_cache_bytes.argtypes = [ctypes.POINTER(KvCacheStruct), ctypes.POINTER(sz), ctypes.POINTER(sz)]
+        L.moe_mxfp4_kv_cache_bytes.restype = ctypes.c_int
+        L.moe_mxfp4_cache_plan.argtypes = [ctypes.POINTER(PlanArgs), P]
+        L.moe_mxfp4_cache_plan.restype = ctypes.c_int
+        L.moe_mxfp4_qk_norm_rope.argtypes = [ctypes.POINTER(RopeArgs), ctypes.POINTER(KvCacheStruct), P]
+        L.moe_mxfp4_qk_norm_rope.restype = ctypes.c_int
+        L.moe_mxfp4_kv_read.argtypes = [ctypes.POINTER(KvCacheStruct), P, i32, P, P, P]
+        L.moe_mxfp4_kv_read.restype = ctypes.c_int
+        L.moe_mxfp4_attention_workspace_bytes.argtypes = [ctypes.POINTER(AttnArgs), ctypes.POINTER(KvCacheStruct)]
+        L.moe_mxfp4_attention_workspace_bytes.restype = sz
+        L.moe_mxfp4_attention.argtypes = [ctypes.POINTER(AttnArgs), ctypes.POINTER(KvCacheStruct), P, sz, P]
+        L.moe_mxfp4_attention.restype = ctypes.c_int
         L.moe_mxfp4_probe.argtypes = [i32, P, sz, i32, P, ctypes.POINTER(ctypes.c_double), P]
         L.moe_mxfp4_probe.restype = ctypes.c_int
         L.moe_mxfp4_stage_timing.argtypes = [P, i32]
@@ -438,6 +488,253 @@ def dflash_accept(draft, p_draft, p_target, u, r, n_accepted=None, next_token=No
                                          _ptr(r), _ptr(n_accepted), _ptr(next_token), _ptr(workspace),
                                          workspace.numel(), _stream(stream)), "moe_mxfp4_dflash_accept")
     return n_accepted, next_token
+
+
+def _like(t, dtype, shape, device, name):
+    """Argument check: a contiguous tensor of this dtype and shape on this CUDA device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _heads(t, D, device, name):
+    """Argument check: bf16 [T, heads, D] on this CUDA device whose heads of a token are contiguous; its token stride."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != D or t.device != device or (
+            t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D))):
+        raise ValueError(f"{name}: expected bfloat16 [T, heads, {D}] on {device} with contiguous heads, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    # the stride between tokens is of no account where there are not two
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+class _On:
+    """The device of a call's tensors and the stream it runs on, both current inside ``with``."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream of {stream.device} for tensors on {device}")
+        own = torch.cuda.current_stream(device)
+        self.stream = own if stream is None else stream
+        # the common case, all of it current already, enters nothing
+        self._ctx = (None if self.stream == own and torch.cuda.current_device() == device.index else
+                     torch.cuda.stream(self.stream))
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+class KvCache:
+    """A paged key/value cache of ``num_pages`` pages of ``page_size`` tokens.
+
+    ``fmt``: ``KV_MXFP4`` (uint8 codes and E8M0 scale bytes) or ``KV_BF16``.
+    The buffers ``k``, ``v`` [pages, kv_heads, page_size, D/2 or D] and
+    ``k_scale``, ``v_scale`` [pages, kv_heads, page_size, D/32] (None for
+    bf16) have the layout of the C header; they start zeroed.  ``wrap`` takes
+    existing buffers.
+    """
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, fmt: int = KV_MXFP4,
+                 device="cuda"):
+        import torch
+        if fmt not in (KV_BF16, KV_MXFP4):
+            raise ValueError(f"fmt: expected KV_BF16 or KV_MXFP4, got {fmt}")
+        shape = (num_pages, kv_heads, page_size)
+        if fmt == KV_BF16:
+            k, v = (torch.zeros((*shape, head_dim), dtype=torch.bfloat16, device=device) for _ in range(2))
+            self._take(k, v, None, None)
+        else:
+            k, v = (torch.zeros((*shape, head_dim // 2), dtype=torch.uint8, device=device) for _ in range(2))
+            ks, vs = (torch.zeros((*shape, head_dim // 32), dtype=torch.uint8, device=device) for _ in range(2))
+            self._take(k, v, ks, vs)
+
+    @classmethod
+    def wrap(cls, k, v, k_scale=None, v_scale=None):
+        self = cls.__new__(cls)
+        self._take(k, v, k_scale, v_scale)
+        return self
+
+    def _take(self, k, v, k_scale, v_scale):
+        import torch
+        fp4 = k_scale is not None
+        if k.dim() != 4:
+            raise ValueError(f"k: expected 4 dimensions, got {tuple(k.shape)}")
+        pages, heads, ps, width = k.shape
+        D = width * 2 if fp4 else width
+        dt = torch.uint8 if fp4 else torch.bfloat16
+        _like(k, dt, k.shape, k.device, "k")
+        _like(v, dt, k.shape, k.device, "v")
+        if fp4:
+            _like(k_scale, torch.uint8, (pages, heads, ps, D // 32), k.device, "k_scale")
+            _like(v_scale, torch.uint8, (pages, heads, ps, D // 32), k.device, "v_scale")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.fmt = KV_MXFP4 if fp4 else KV_BF16
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, ps, D
+        self.device = k.device
+        self.struct = KvCacheStruct(ctypes.sizeof(KvCacheStruct), self.fmt, pages, ps, heads, D, _ptr(k), _ptr(v),
+                                    _ptr(k_scale), _ptr(v_scale))
+        data, scale = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(lib().moe_mxfp4_kv_cache_bytes(ctypes.byref(self.struct), ctypes.byref(data), ctypes.byref(scale)),
+               "moe_mxfp4_kv_cache_bytes")
+
+
+CachePlan = collections.namedtuple("CachePlan", "cu_q kv_lens slots positions refused held free_state")
+
+
+def cache_plan(ctx_lens, new_lens, block_table, held, free_ring, free_state, *, page_size: int, num_tokens: int,
+               held_out=None, free_out=None, out: CachePlan | None = None, stream=None) -> CachePlan:
+    """Block tables and slot map of a step, from request lengths (moe_mxfp4_cache_plan).
+
+    int32 CUDA tensors: ctx_lens, new_lens, held [B], block_table [B, max_blocks]
+    and free_ring [num_pages] (both updated), free_state [2].  ``held_out``
+    and ``free_out`` receive the state after the call and must not be the
+    inputs; ``out``: an earlier result whose tensors are used again.
+    """
+    import torch
+    i32, dev = torch.int32, block_table.device
+    B, W = block_table.shape
+    N = free_ring.numel()
+    with _On(dev, stream) as st:
+        if out is None:
+            out = CachePlan(torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
+                            torch.empty(num_tokens, dtype=i32, device=dev),
+                            torch.empty(num_tokens, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev),
+                            torch.empty(B, dtype=i32, device=dev) if held_out is None else held_out,
+                            torch.empty(2, dtype=i32, device=dev) if free_out is None else free_out)
+        elif held_out is not None or free_out is not None:
+            out = out._replace(**{n: t for n, t in (("held", held_out), ("free_state", free_out)) if t is not None})
+        for t, shape, name in ((ctx_lens, (B,), "ctx_lens"), (new_lens, (B,), "new_lens"), (held, (B,), "held"),
+                               (block_table, (B, W), "block_table"), (free_ring, (N,), "free_ring"),
+                               (free_state, (2,), "free_state"), (out.cu_q, (B + 1,), "cu_q"),
+                               (out.kv_lens, (B,), "kv_lens"), (out.slots, (num_tokens,), "slots"),
+                               (out.positions, (num_tokens,), "positions"), (out.refused, (1,), "refused"),
+                               (out.held, (B,), "held_out"), (out.free_state, (2,), "free_out")):
+            _like(t, i32, shape, dev, name)
+        args = PlanArgs(ctypes.sizeof(PlanArgs), B, num_tokens, W, page_size, N,
+                        *[t.data_ptr() for t in (ctx_lens, new_lens, block_table, held, out.held, free_ring,
+                                                 free_state, out.free_state, out.cu_q, out.kv_lens, out.slots,
+                                                 out.positions, out.refused)])
+        _check(lib().moe_mxfp4_cache_plan(ctypes.byref(args), st), "moe_mxfp4_cache_plan")
+    return out
+
+
+def qk_norm_rope(q, k, v, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, cache: KvCache | None = None, slots=None, q_out=None, k_out=None,
+                 stream=None):
+    """Per-head norms, rotation and cache write (moe_mxfp4_qk_norm_rope) -> (q_out, k_out).
+
+    q [T, heads, D], k, v [T, kv_heads, D]: bf16 CUDA, tokens at any stride
+    that is a multiple of 8.  inv_freq: float64 [rot_dim/2].  With ``cache``
+    the key and value go to ``slots`` (int32 [T]) and k_out is None unless
+    given; without one, v and slots are ignored.
+    """
+    import torch
+    dev = q.device
+    T, H, D = q.shape
+    HK = k.shape[1]
+    qs, ks = _heads(q, D, dev, "q"), _heads(k, D, dev, "k")
+    vs = 0
+    if k.shape[0] != T:
+        raise ValueError(f"k: {k.shape[0]} tokens, q has {T}")
+    _like(positions, torch.int32, (T,), dev, "positions")
+    _like(inv_freq, torch.float64, (inv_freq.numel(),), dev, "inv_freq")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _like(w, torch.bfloat16, (D,), dev, name)
+    if cache is not None:
+        vs = _heads(v, D, dev, "v")
+        if v.shape != k.shape or slots is None:
+            raise ValueError("a cache write needs v of k's shape, and slots")
+        _like(slots, torch.int32, (T,), dev, "slots")
+        if cache.device != dev:
+            raise ValueError(f"cache on {cache.device}, q on {dev}")
+    with _On(dev, stream) as st:
+        if q_out is None:
+            q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _like(q_out, torch.bfloat16, (T, H, D), dev, "q_out")
+        if k_out is not None:
+            _like(k_out, torch.bfloat16, (T, HK, D), dev, "k_out")
+        elif cache is None:
+            k_out = torch.empty((T, HK, D), dtype=torch.bfloat16, device=dev)
+        args = RopeArgs(ctypes.sizeof(RopeArgs), T, H, HK, D, 2 * inv_freq.numel(), int(interleaved), eps, qs, ks, vs,
+                        q.data_ptr(), k.data_ptr(), None if cache is None else v.data_ptr(),
+                        None if q_weight is None else q_weight.data_ptr(),
+                        None if k_weight is None else k_weight.data_ptr(), inv_freq.data_ptr(), positions.data_ptr(),
+                        None if cache is None else slots.data_ptr(), q_out.data_ptr(),
+                        None if k_out is None else k_out.data_ptr())
+        _check(lib().moe_mxfp4_qk_norm_rope(ctypes.byref(args), None if cache is None else ctypes.byref(cache.struct),
+                                            st), "moe_mxfp4_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_read(cache: KvCache, slots, stream=None):
+    """The values a cache holds at ``slots`` (int32 [n]): (k, v) bf16 [n, kv_heads, D] (moe_mxfp4_kv_read)."""
+    import torch
+    n, dev = slots.numel(), cache.device
+    _like(slots, torch.int32, (n,), dev, "slots")
+    with _On(dev, stream) as st:
+        k, v = (torch.empty((n, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        _check(lib().moe_mxfp4_kv_read(ctypes.byref(cache.struct), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
+                                       st), "moe_mxfp4_kv_read")
+    return k, v
+
+
+def attention(q, cache: KvCache, block_table, cu_q, kv_lens, *, max_q: int, max_kv: int, scale: float | None = None,
+              causal: bool = True, window: int = 0, sinks: int = 0, out=None, workspace=None, stream=None):
+    """Attention of packed rows over a paged cache (moe_mxfp4_attention) -> out [T, heads, D] bf16.
+
+    q bf16 [T, heads, D]; block_table int32 [B, max_blocks], cu_q int32 [B+1],
+    kv_lens int32 [B], all CUDA.  ``max_q`` and ``max_kv``: the longest
+    sequences the caller expects (longer ones are slower, not wrong).
+    ``scale``: 1/sqrt(D) by default.  ``window`` > 0: only the last ``window``
+    keys, and the first ``sinks``, are visible.  Rows of ``out`` past cu_q[B]
+    are not written (unspecified where ``out`` is made here).
+    """
+    import torch
+    dev = q.device
+    T, H, D = q.shape
+    B, W = block_table.shape
+    qs = _heads(q, D, dev, "q")
+    _like(block_table, torch.int32, (B, W), dev, "block_table")
+    _like(cu_q, torch.int32, (B + 1,), dev, "cu_q")
+    _like(kv_lens, torch.int32, (B,), dev, "kv_lens")
+    if cache.head_dim != D or cache.device != dev:
+        raise ValueError(f"q has heads of {D} on {dev}, the cache of {cache.head_dim} on {cache.device}")
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+        elif out.shape != q.shape:
+            raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
+        args = AttnArgs(ctypes.sizeof(AttnArgs), B, T, H, max_q, max_kv, W, int(causal), window, sinks,
+                        D ** -0.5 if scale is None else scale, qs, _heads(out, D, dev, "out"), q.data_ptr(),
+                        out.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr())
+        L, a, c = lib(), ctypes.byref(args), ctypes.byref(cache.struct)
+        if workspace is None:
+            need = L.moe_mxfp4_attention_workspace_bytes(a, c)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        elif workspace.device != dev:
+            raise ValueError(f"workspace on {workspace.device}, q on {dev}")
+        _check(L.moe_mxfp4_attention(a, c, _ptr(workspace), 0 if workspace is None else workspace.numel() *
+                                     workspace.element_size(), st), "moe_mxfp4_attention")
+    return out
+
+
+def attention_workspace_bytes(cache: KvCache, num_tokens: int, heads: int, batch: int, *, max_q: int, max_kv: int,
+                              window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace an ``attention`` call of these sizes needs (0: none)."""
+    row = heads * cache.head_dim
+    args = AttnArgs(ctypes.sizeof(AttnArgs), batch, num_tokens, heads, max_q, max_kv, 1, 1, window, sinks, 1.0, row, row)
+    return lib().moe_mxfp4_attention_workspace_bytes(ctypes.byref(args), ctypes.byref(cache.struct))
 
 
 PROBE_STREAM, PROBE_MFMA_BF16, PROBE_MFMA_FP8_FP4, PROBE_MFMA_FP4_FP4 = 0, 1, 2, 3

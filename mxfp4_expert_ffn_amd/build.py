@@ -11,7 +11,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_mxfp4.so")
 SOURCES = ["api.hip", "router.hip", "dflash.hip", "probes.hip", "route_sort.hip", "expert_gemm.hip", "fused.hip", "dense_gemm.hip", "combine.hip",
-           "quant_act.hip"]
+           "quant_act.hip", "kv_plan.hip", "qk_rope.hip", "attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-FP32 VALU forms are disabled for all device code (see DESIGN notes on

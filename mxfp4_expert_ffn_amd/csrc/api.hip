@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -18,6 +19,7 @@
 #include <new>
 #include <vector>
 
+#include "kv_cache.hpp"
 #include "layer.hpp"
 
 struct moe_mxfp4_ctx {
@@ -89,7 +91,7 @@ Layout make_layout(const moe_mxfp4_config& c, int64_t T) {
 // to a launch site's name, a call that reaches that site returns MOE_ERR_HIP
 // there instead of launching, as a failed launch would.  Sites: router,
 // route (the routing or fused routing + permutation launch), sort, quant,
-// gateup, down, combine, dflash.  Read on every call, so a test can set and
+// gateup, down, combine, dflash, plan, rope, kvread, attn.  Read on every call, so a test can set and
 // clear it between calls.
 bool fault_at(const char* site) {
     const char* e = std::getenv("MOE_MXFP4_FAULT");
@@ -727,6 +729,163 @@ moe_status moe_mxfp4_tile_weights(const uint8_t* packed, const uint8_t* scales, 
     if (rows == 0) return MOE_OK;
     if (moe::launch_tile(packed, scales, rows, K, tiled_packed, tiled_scales,
                          static_cast<hipStream_t>(hip_stream)) != hipSuccess)
+        return MOE_ERR_HIP;
+    return MOE_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes of a cache (its pointers are not looked at).
+moe_status check_kv_sizes(const moe_mxfp4_kv_cache* c) {
+    if (!c || c->struct_size != sizeof(moe_mxfp4_kv_cache)) return MOE_ERR_INVALID_ARG;
+    if (c->format != MOE_KV_BF16 && c->format != MOE_KV_MXFP4) return MOE_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1) return MOE_ERR_INVALID_ARG;
+    if (!moe::kv_page_size_ok(c->page_size) || (c->head_dim != 64 && c->head_dim != 128) ||
+        c->kv_heads > moe::kKvMaxHeads || (int64_t)c->num_pages * c->page_size >= (int64_t)1 << 31)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+moe_status check_kv_cache(const moe_mxfp4_kv_cache* c) {
+    const moe_status st = check_kv_sizes(c);
+    if (st != MOE_OK) return st;
+    const bool fp4 = c->format == MOE_KV_MXFP4;
+    if (!c->k || !c->v || (fp4 && (!c->k_scale || !c->v_scale))) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v) || (fp4 && (!aligned16(c->k_scale) || !aligned16(c->v_scale))))
+        return MOE_ERR_ALIGNMENT;
+    return MOE_OK;
+}
+
+// Sizes of an attention call.
+moe_status check_attn_sizes(const moe_mxfp4_attn_args* a, const moe_mxfp4_kv_cache* c) {
+    if (!a || a->struct_size != sizeof(moe_mxfp4_attn_args)) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_kv_sizes(c);
+    if (st != MOE_OK) return st;
+    if (a->batch < 0 || a->num_tokens < 0 || a->heads < 1 || a->max_q < 1 || a->max_kv < 1 || a->max_blocks < 1 ||
+        a->window < 0 || a->sinks < 0 || (a->sinks > 0 && a->window == 0) || !(a->scale > 0.f) ||
+        !std::isfinite(a->scale) || a->heads % c->kv_heads != 0)
+        return MOE_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)a->heads * c->head_dim;
+    if (a->q_stride < row || a->q_stride % 8 != 0 || a->out_stride < row || a->out_stride % 8 != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (a->batch > 65535 || a->heads > 16384 || (int64_t)a->num_tokens * a->heads >= (int64_t)1 << 30 ||
+        (int64_t)a->batch * c->kv_heads > (int64_t)1 << 20)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_mxfp4_kv_cache_bytes(const moe_mxfp4_kv_cache* cache, size_t* data_bytes, size_t* scale_bytes) {
+    if (!data_bytes || !scale_bytes) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_kv_sizes(cache);
+    if (st != MOE_OK) return st;
+    const size_t rows = (size_t)cache->num_pages * cache->page_size * cache->kv_heads;
+    const bool fp4 = cache->format == MOE_KV_MXFP4;
+    *data_bytes = rows * (fp4 ? cache->head_dim / 2 : cache->head_dim * 2);
+    *scale_bytes = fp4 ? rows * (cache->head_dim / MOE_MXFP4_BLOCK) : 0;
+    return MOE_OK;
+}
+
+moe_status moe_mxfp4_cache_plan(const moe_mxfp4_plan_args* a, void* hip_stream) {
+    if (!a || a->struct_size != sizeof(moe_mxfp4_plan_args)) return MOE_ERR_INVALID_ARG;
+    if (a->batch < 0 || a->num_tokens < 0 || a->max_blocks < 1 || a->page_size < 1 || a->num_pages < 1)
+        return MOE_ERR_INVALID_ARG;
+    if (!moe::kv_page_size_ok(a->page_size) || a->batch > moe::kPlanMaxBatch || a->num_tokens > 1 << 30 ||
+        (int64_t)a->num_pages * a->page_size >= (int64_t)1 << 31 ||
+        (int64_t)a->max_blocks * a->page_size >= (int64_t)1 << 31)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    const void* always[] = {a->free_ring, a->free_state, a->free_state_out, a->cu_q, a->refused};
+    const void* per_request[] = {a->ctx_lens, a->new_lens, a->block_table, a->held, a->held_out, a->kv_lens};
+    const void* per_row[] = {a->slots, a->positions};
+    for (const void* p : always)
+        if (!p) return MOE_ERR_INVALID_ARG;
+    for (const void* p : per_request)
+        if (a->batch > 0 && !p) return MOE_ERR_INVALID_ARG;
+    for (const void* p : per_row)
+        if (a->num_tokens > 0 && !p) return MOE_ERR_INVALID_ARG;
+    if (a->free_state == a->free_state_out || (a->batch > 0 && a->held == a->held_out)) return MOE_ERR_INVALID_ARG;
+    for (const void* p : always)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    for (const void* p : per_request)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    for (const void* p : per_row)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    if (fault_at("plan") || moe::launch_cache_plan(*a, static_cast<hipStream_t>(hip_stream)) != hipSuccess)
+        return MOE_ERR_HIP;
+    return MOE_OK;
+}
+
+moe_status moe_mxfp4_qk_norm_rope(const moe_mxfp4_rope_args* a, const moe_mxfp4_kv_cache* cache, void* hip_stream) {
+    if (!a || a->struct_size != sizeof(moe_mxfp4_rope_args)) return MOE_ERR_INVALID_ARG;
+    if (a->num_tokens < 0 || a->heads < 1 || a->kv_heads < 1 || a->head_dim < 1 || a->rot_dim < 0 ||
+        a->rot_dim > a->head_dim || !(a->eps >= 0.f) || !std::isfinite(a->eps))
+        return MOE_ERR_INVALID_ARG;
+    if ((a->head_dim != 64 && a->head_dim != 128) || a->rot_dim % 16 != 0 || a->heads > moe::kKvMaxHeads ||
+        a->kv_heads > moe::kKvMaxHeads || a->num_tokens >= 1 << 24)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    const int64_t qrow = (int64_t)a->heads * a->head_dim, krow = (int64_t)a->kv_heads * a->head_dim;
+    if (a->q_stride < qrow || a->k_stride < krow || a->q_stride % 8 != 0 || a->k_stride % 8 != 0 ||
+        (cache && (a->v_stride < krow || a->v_stride % 8 != 0)))
+        return MOE_ERR_INVALID_ARG;
+    if (cache) {
+        const moe_status st = check_kv_cache(cache);
+        if (st != MOE_OK) return st;
+        if (cache->kv_heads != a->kv_heads || cache->head_dim != a->head_dim) return MOE_ERR_INVALID_ARG;
+    }
+    if (a->num_tokens == 0) return MOE_OK;
+    if (!a->q || !a->k || !a->positions || !a->q_out || (a->rot_dim > 0 && !a->inv_freq) ||
+        (cache ? !a->v || !a->slots : !a->k_out))
+        return MOE_ERR_INVALID_ARG;
+    // an output may be its own input where the rows coincide
+    if ((a->q_out == a->q && a->q_stride != qrow) || (a->k_out == a->k && a->k_stride != krow))
+        return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {a->q, a->k, cache ? a->v : nullptr, a->q_weight, a->k_weight, a->inv_freq, a->positions,
+                          cache ? a->slots : nullptr, a->q_out, a->k_out};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    if (fault_at("rope") || moe::launch_qk_norm_rope(*a, cache, static_cast<hipStream_t>(hip_stream)) != hipSuccess)
+        return MOE_ERR_HIP;
+    return MOE_OK;
+}
+
+moe_status moe_mxfp4_kv_read(const moe_mxfp4_kv_cache* cache, const int32_t* slots, int32_t n, void* k, void* v,
+                             void* hip_stream) {
+    const moe_status st = check_kv_cache(cache);
+    if (st != MOE_OK) return st;
+    if (n < 0) return MOE_ERR_INVALID_ARG;
+    if ((int64_t)n * cache->kv_heads >= (int64_t)1 << 28) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (n == 0) return MOE_OK;
+    if (!slots || (!k && !v)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(slots) || !aligned16(k) || !aligned16(v)) return MOE_ERR_ALIGNMENT;
+    if (fault_at("kvread") ||
+        moe::launch_kv_read(*cache, slots, n, k, v, static_cast<hipStream_t>(hip_stream)) != hipSuccess)
+        return MOE_ERR_HIP;
+    return MOE_OK;
+}
+
+size_t moe_mxfp4_attention_workspace_bytes(const moe_mxfp4_attn_args* args, const moe_mxfp4_kv_cache* cache) {
+    if (check_attn_sizes(args, cache) != MOE_OK || args->batch == 0 || args->num_tokens == 0) return 0;
+    return moe::attention_workspace_bytes(*args, *cache);
+}
+
+moe_status moe_mxfp4_attention(const moe_mxfp4_attn_args* a, const moe_mxfp4_kv_cache* cache, void* workspace,
+                               size_t workspace_bytes, void* hip_stream) {
+    moe_status st = check_attn_sizes(a, cache);
+    if (st == MOE_OK) st = check_kv_cache(cache);
+    if (st != MOE_OK) return st;
+    if (a->batch == 0 || a->num_tokens == 0) return MOE_OK;
+    if (!a->q || !a->out || a->q == a->out || !a->block_table || !a->cu_q || !a->kv_lens) return MOE_ERR_INVALID_ARG;
+    const void* ptrs[] = {a->q, a->out, a->block_table, a->cu_q, a->kv_lens, workspace};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return MOE_ERR_ALIGNMENT;
+    const size_t need = moe::attention_workspace_bytes(*a, *cache);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+    if (fault_at("attn") || moe::launch_attention(*a, *cache, workspace, static_cast<hipStream_t>(hip_stream)) != hipSuccess)
         return MOE_ERR_HIP;
     return MOE_OK;
 }
