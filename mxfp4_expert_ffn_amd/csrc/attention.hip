@@ -46,10 +46,11 @@ struct AttnArgs {
     uint16_t* out;
     const int32_t *table, *cu_q, *kv_lens;
     const uint8_t *k, *v, *ks, *vs;
-    float *part, *stat;                            // sums [T H][nsplit][D], (reference, sum of weights) [T H][nsplit][2]
+    float *part, *stat;                            // pieces: sums [workgroup][2][rows][D], (reference, sum of weights)
+    int64_t* start;                                // [B + 2]: first unit of each sequence per head, and the quota
     int64_t qs, os;
     int32_t B, T, H, Hk, G, W, shift, num_pages, causal, window, sinks;
-    int32_t share, nsplit, row_tiles;              // tiles per workgroup; workgroups along the keys, along the rows
+    int32_t row_tiles;                             // even: workgroups along the rows of a sequence and head
     float c;                                       // scale * log2(e)
 };
 
@@ -57,11 +58,14 @@ struct AttnArgs {
 struct Seq {
     int start, n, kv;
 };
-__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+// Arrays read through the scalar cache.
+typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
+template <typename Ints>
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, Ints cu_q, Ints kv_lens) {
     Seq s;
-    s.start = min(max(a.cu_q[b], 0), a.T);
-    s.n = min(max(a.cu_q[b + 1], s.start), a.T) - s.start;
-    s.kv = (int)min((int64_t)max(a.kv_lens[b], 0), (int64_t)a.W << a.shift);
+    s.start = min(max(cu_q[b], 0), a.T);
+    s.n = min(max(cu_q[b + 1], s.start), a.T) - s.start;
+    s.kv = (int)min((int64_t)max(kv_lens[b], 0), (int64_t)a.W << a.shift);
     return s;
 }
 
@@ -96,6 +100,30 @@ template <int D> struct Raw<MOE_KV_BF16, D> {
     uint32_t v[8][D / 32];
 };
 
+// Keeps the compiler from moving the decoding of V out of a loop, where the
+// decoded tile would take registers from the common path.
+template <int D>
+__device__ __forceinline__ void decode_anew(Raw<MOE_KV_MXFP4, D>& r) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(r.v[i]));
+}
+template <int D>
+__device__ __forceinline__ void decode_anew(Raw<MOE_KV_BF16, D>& r) {
+#pragma unroll
+    for (int i = 0; i < 8 * (D / 32); ++i) asm volatile("" : "+v"(r.v[i / (D / 32)][i % (D / 32)]));
+}
+
+// A tile of 32 keys in LDS as a wave fetches it: keys, values and (MXFP4)
+// their scales, in the cache's order but for a permutation of the 16-byte
+// chunks of a key row, chosen so that the 16 lanes that read the same chunk
+// of 16 rows find it in different banks.
+template <int FMT, int D> struct Tile {
+    static constexpr int kRowBytes = FMT == MOE_KV_MXFP4 ? D / 2 : D * 2;
+    static constexpr int kKeys = 0, kValues = kTile * kRowBytes, kScales = 2 * kValues;
+    static constexpr int kBytes = kScales + (FMT == MOE_KV_MXFP4 ? 256 : 0);
+    static constexpr int kFetches = 2 * kValues / 1024 + (FMT == MOE_KV_MXFP4 ? 1 : 0);   // loads of a wave
+};
+
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* src) {
     if constexpr (N % 4 == 0) {
@@ -114,50 +142,127 @@ __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* src) {
 // Pages of a tile's two halves of 16 keys; -1: outside the cache or behind the
 // last key.
 struct Pages {
-    int p[2];
-};
-__device__ __forceinline__ Pages pages_of(const AttnArgs& a, const int32_t* row, int tile, int kv) {
-    Pages pg;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int key = tile * kTile + 16 * h;
-        int p = -1;
-        if (key < kv) p = row[key >> a.shift];     // key < kv <= W pages
-        pg.p[h] = p >= 0 && p < a.num_pages ? p : -1;
+    int a, b;
+    __device__ __forceinline__ int of(bool first) const {
+        const int x = a, y = b;                    // values: a choice between the members would keep them in memory
+        return first ? x : y;
     }
-    return pg;
+};
+// The table is read through the scalar cache: vector loads return in order,
+// so a page looked up that way would wait for the tiles asked for before it.
+__device__ __forceinline__ Pages pages_of(const AttnArgs& a, ScalarInts row, int tile, int kv) {
+    auto look = [&](int key) {
+        const int p = row[min(key, kv - 1) >> a.shift];                 // kv <= W pages
+        return key < kv && (unsigned)p < (unsigned)a.num_pages ? p : -1;
+    };
+    return Pages{look(tile * kTile), look(tile * kTile + 16)};
+}
+
+// 16 (or 4) bytes per lane from base + off (base the same for all lanes)
+// straight into LDS: lane L's go to lds + 16 L (4 L).  These loads write no
+// register, so nothing the compiler allocates can be under way; it does not
+// count them either, which is the point: of a ring slot chosen at run time it
+// would assume that any load under way may write it, and wait for all of them
+// before a read.  wait_loads() below does the waiting, before every read.
+// ONCE: no other wave reads these bytes, so they need not stay in the caches
+// (nt): 5.6 against 4.7 TB/s of such loads alone over 0.7 GB of MXFP4 keys.
+template <bool ONCE>
+__device__ __forceinline__ void lds_dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
+    if constexpr (ONCE)
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(off), "s"(base)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                     : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma16(const uint8_t* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma4(const uint8_t* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+}
+
+// Starts the loads of a tile into its slot dst (an LDS address, the same for
+// all lanes).  What this wave read from the slot before has arrived.
+template <int FMT, int D, bool ONCE>
+__device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pages& pg, int tile, int hk, int lane) {
+    using T = Tile<FMT, D>;
+    const int mask = (1 << a.shift) - 1;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // first row of each half; page 0 stands in for none: read, then not used
+    const int64_t b0 = (((int64_t)max(pg.a, 0) * a.Hk + hk) << a.shift) + ((tile * kTile) & mask);
+    const int64_t b1 = (((int64_t)max(pg.b, 0) * a.Hk + hk) << a.shift) + ((tile * kTile + 16) & mask);
+    if constexpr (FMT == MOE_KV_MXFP4 && D == 128) {
+        // chunk c of row r is stored at c ^ (r / 8)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            lds_dma16<ONCE>(a.k + (h ? b1 : b0) * 64, lane / 4 * 64 + ((lane % 4) ^ (2 * h + lane / 32)) * 16, dst + h * 1024);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) lds_dma16<ONCE>(a.v + (h ? b1 : b0) * 64, lane * 16, dst + T::kValues + h * 1024);
+        const uint8_t* sc = lane < 32 ? a.ks : a.vs;
+        lds_dma4(sc + (lane & 16 ? b1 : b0) * 4 + lane % 16 * 4, dst + T::kScales);
+    } else if constexpr (FMT == MOE_KV_MXFP4) {
+        const int64_t base = lane < 32 ? b0 : b1;
+        const int chunk = (lane % 2) ^ ((lane / 16) & 1);               // chunk c of row r at c ^ (r / 8 mod 2)
+        lds_dma16(a.k + base * 32 + (lane / 2 % 16 * 32 + chunk * 16), dst);
+        lds_dma16(a.v + base * 32 + lane % 32 * 16, dst + T::kValues);
+        const uint8_t* sc = lane & 16 ? a.vs : a.ks;                    // lanes 32.. repeat lanes 0..31
+        lds_dma4(sc + (lane & 8 ? b1 : b0) * 2 + lane % 8 * 4, dst + T::kScales);
+    } else {
+        constexpr int C = D / 8, R = 64 / C;                            // chunks per row, rows per load
+#pragma unroll
+        for (int i = 0; i < kTile / R; ++i) {
+            // chunk c of row r at c ^ (its lane m = 4 (r / 8) + r mod 4)
+            const int row = i * R + lane / C, mm = 4 * (row / 8) + row % 4;
+            lds_dma16<ONCE>(a.k + (i < 16 / R ? b0 : b1) * (2 * D), row % 16 * (2 * D) + ((lane % C) ^ (mm % C)) * 16, dst + i * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < kTile / R; ++i)
+            lds_dma16<ONCE>(a.v + (i < 16 / R ? b0 : b1) * (2 * D) + i % (16 / R) * 1024, lane * 16, dst + T::kValues + i * 1024);
+    }
+}
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// Waits until at most N loads of this wave are under way (they end in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 template <int FMT, int D>
-__device__ __forceinline__ void load_tile(Raw<FMT, D>& r, const AttnArgs& a, const Pages& pg, int tile, int hk, int lane) {
+__device__ __forceinline__ void read_keys(Raw<FMT, D>& r, const uint8_t* src, int lane) {
     const int m = lane % 16, g = lane / 16;
-    const int mask = (1 << a.shift) - 1;
-    const int pa = max(pg.p[0], 0), pb = max(pg.p[1], 0);               // page 0 stands in: read, then not used
-    const int64_t ka = ((int64_t)(m < 8 ? pa : pb) * a.Hk + hk) << a.shift;
-    const int64_t va = ((int64_t)(g < 2 ? pa : pb) * a.Hk + hk) << a.shift;
-    const int vrow = (tile * kTile + 8 * g) & mask;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int64_t row = ka + ((tile * kTile + 8 * (m / 4) + 4 * t + m % 4) & mask);
+        const int row = 8 * (m / 4) + 4 * t + m % 4;
+        const uint8_t* p = src + row * Tile<FMT, D>::kRowBytes;
         if constexpr (FMT == MOE_KV_MXFP4) {
-            load_words<D / 32>(r.k[t], a.k + row * (D / 2) + g * (D / 8));
-            r.kb[t] = a.ks[row * (D / 32) + g * D / 128];
+            if constexpr (D == 128) load_words<4>(r.k[t], p + (g ^ (m / 4)) * 16);
+            else load_words<2>(r.k[t], p + ((g / 2) ^ ((m / 4) & 1)) * 16 + g % 2 * 8);
+            r.kb[t] = src[Tile<FMT, D>::kScales + row * (D / 32) + g * D / 128];
         } else {
-            const u32x4_t* src = reinterpret_cast<const u32x4_t*>(a.k + (row * D + g * (D / 4)) * 2);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) r.k[t][i] = src[i];
+            for (int i = 0; i < D / 32; ++i)
+                r.k[t][i] = *reinterpret_cast<const u32x4_t*>(p + ((g * (D / 32) + i) ^ (m % (D / 8))) * 16);
         }
     }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void read_values(Raw<FMT, D>& r, const uint8_t* src, int lane) {
+    using T = Tile<FMT, D>;
+    const int m = lane % 16, g = lane / 16;
     if constexpr (FMT == MOE_KV_MXFP4) {
         constexpr int KG = v_keys_per_piece(D);
 #pragma unroll
-        for (int i = 0; i < 8 / KG; ++i)
-            load_words<4>(r.v + 4 * i, a.v + va * (D / 2) + (vrow / KG + i) * (KG * D / 2) + m * 16);
-        const uint2 b = *reinterpret_cast<const uint2*>(a.vs + va * (D / 32) + vrow * (D / 32) + (m * D / 512) * 8);
+        for (int i = 0; i < 8 / KG; ++i) load_words<4>(r.v + 4 * i, src + T::kValues + ((8 / KG) * g + i) * 256 + m * 16);
+        const uint2 b = *reinterpret_cast<const uint2*>(src + T::kScales + kTile * (D / 32) + (g * (D / 32) + m * D / 512) * 8);
         r.vb[0] = b.x; r.vb[1] = b.y;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) load_words<D / 32>(r.v[j], a.v + ((va + vrow + j) * D + m * (D / 16)) * 2);
+        for (int j = 0; j < 8; ++j) load_words<D / 32>(r.v[j], src + T::kValues + (8 * g + j) * (2 * D) + m * (D / 8));
     }
 }
 
@@ -182,7 +287,10 @@ __device__ __forceinline__ void v_operand(const Raw<FMT, D>& r, uint32_t live, b
     if constexpr (FMT == MOE_KV_MXFP4) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float sc = e8m0_as_scale((r.vb[j / 4] >> (8 * (j % 4))) & 0xFF);
+            // the convert reads the exponent field of its scale only, so the
+            // other bytes around it may stay
+            const uint32_t b = r.vb[j / 4];
+            const float sc = __uint_as_float(j % 4 == 3 ? b >> 1 : b << (23 - 8 * (j % 4)));
             const int at = j * (D / 32) + U;       // byte of the lane's codes
             const uint32_t word = r.v[at / 4];
             w[j] = at % 4 == 0 ? decode2<0>(word, sc) : at % 4 == 1 ? decode2<1>(word, sc)
@@ -192,10 +300,8 @@ __device__ __forceinline__ void v_operand(const Raw<FMT, D>& r, uint32_t live, b
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[j] = r.v[j][U];
     }
-    if (live != 0xFF) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = (live >> j) & 1 ? w[j] : 0;
-    }
+    for (int j = 0; j < 8; ++j) w[j] = (live >> j) & 1 ? w[j] : 0;     // nothing where live is the constant 0xFF
     u32x4_t lo, hi;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -206,15 +312,11 @@ __device__ __forceinline__ void v_operand(const Raw<FMT, D>& r, uint32_t live, b
     second = __builtin_bit_cast(bf16x8_t, hi);
 }
 
-__device__ __forceinline__ bool wild_pair(uint32_t w) {                 // infinite or NaN bf16 in either half
-    return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-
 // Whether a live key of this lane has an infinite or NaN value (MXFP4: a
 // scale with which 6 passes float32's range, or NaN).
 template <int FMT, int D>
 __device__ __forceinline__ bool wild_values(const Raw<FMT, D>& r, uint32_t live) {
-    bool wild = false;
+    uint32_t wild = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         bool x = false;
@@ -222,26 +324,16 @@ __device__ __forceinline__ bool wild_values(const Raw<FMT, D>& r, uint32_t live)
             x = ((r.vb[j / 4] >> (8 * (j % 4))) & 0xFF) >= 253;
         } else {
 #pragma unroll
-            for (int u = 0; u < D / 32; ++u) x |= wild_pair(r.v[j][u]);
+            for (int u = 0; u < D / 32; ++u)
+                x |= (r.v[j][u] & 0x7F80u) == 0x7F80u || (r.v[j][u] & 0x7F800000u) == 0x7F800000u;
         }
-        wild |= x && ((live >> j) & 1);
+        wild |= (uint32_t)x << j;
     }
-    return wild;
+    return (wild & live) != 0;
 }
 
-// One element of a cached value, as the operands decode it.
-template <int FMT, int D>
-__device__ __forceinline__ float value_at(const AttnArgs& a, int64_t base, int row, int d) {
-    if constexpr (FMT == MOE_KV_BF16) {
-        return bf16_to_f32(reinterpret_cast<const uint16_t*>(a.v)[(base + row) * D + d]);
-    } else {
-        constexpr int KG = v_keys_per_piece(D), C = D / 32;
-        const int byte = d / 2;
-        const uint32_t w = a.v[base * (D / 2) + (row / KG) * (KG * D / 2) + (byte / C) * 16 + (row % KG) * C + byte % C];
-        const uint32_t sb = a.vs[base * C + (row / 8) * (8 * C) + (d / 32) * 8 + row % 8];
-        const uint32_t pair = decode2<0>(w, e8m0_as_scale(sb));
-        return __uint_as_float(d & 1 ? pair & 0xFFFF0000u : pair << 16);
-    }
+__device__ __forceinline__ f32x4_t mfma(const bf16x8_t& x, const bf16x8_t& y, const f32x4_t& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
 }
 
 // What a row sees: keys j < up with j >= lo or j < sinks (none if up <= 0).
@@ -256,37 +348,315 @@ __device__ __forceinline__ uint32_t pack_bf16(float x, float y) {
     return __builtin_bit_cast(uint32_t, r);
 }
 
-// MT tiles of 16 rows per wave.
-template <int FMT, int D, int MT>
-__global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
-    constexpr int NT = D / 16, KS = D / 32, ROWS = 16 * MT;
-    __shared__ float sh_o[kWaves][16][D + 4];
-    __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
-    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int m = lane % 16, g = lane / 16;
-    int id = blockIdx.x;
-    const int rt0 = id % a.row_tiles; id /= a.row_tiles;
-    const int split = id % a.nsplit; id /= a.nsplit;
-    const int hk = id % a.Hk, b = id / a.Hk;
-    const Seq sq = sequence(a, b);
-    const int32_t* trow = a.table + (size_t)b * a.W;
-    const int rows = sq.n * a.G;                   // (token, head of the group) pairs, token-major
+// The lowest n of 8 bits, n clamped to 0..8.
+__device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 8)) - 1; }
 
-    for (int r0 = rt0 * ROWS; r0 < rows; r0 += a.row_tiles * ROWS) {
+// A wave's running softmax of MT tiles of 16 rows.
+template <int D, int MT>
+struct Sums {
+    f32x4_t o[MT][D / 16];                         // O^T
+    f32x4_t l[MT];                                 // the weights' sum, the same in all four
+    float m[MT];                                   // the reference, of row lane % 16
+};
+
+// The eight V^T operands of a tile, each handed to f(number, operand).
+template <int FMT, int D, typename F>
+__device__ __forceinline__ void each_v(const Raw<FMT, D>& r, uint32_t live, F f) {
+    auto pair = [&](auto U) {
+        bf16x8_t x, y;
+        v_operand<FMT, D, decltype(U)::value>(r, live, x, y);
+        f(2 * decltype(U)::value, x);
+        f(2 * decltype(U)::value + 1, y);
+    };
+    pair(std::integral_constant<int, 0>{});
+    pair(std::integral_constant<int, 1>{});
+    if constexpr (D == 128) {
+        pair(std::integral_constant<int, 2>{});
+        pair(std::integral_constant<int, 3>{});
+    }
+}
+
+template <int FMT, int D, int MT>
+__device__ __forceinline__ void scores(f32x4_t (&sc)[MT][2], const Raw<FMT, D>& r, const bf16x8_t (&qf)[MT][D / 32]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int q = 0; q < MT; ++q) sc[q][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s) {
+            const bf16x8_t kf = k_operand<FMT, D>(r, t, s);
+#pragma unroll
+            for (int q = 0; q < MT; ++q) sc[q][t] = mfma(kf, qf[q][s], sc[q][t]);
+        }
+    }
+}
+
+// This lane's largest score of each row, in the exponent's units.
+template <int MT>
+__device__ __forceinline__ void tops(float (&t)[MT], const f32x4_t (&sc)[MT][2], float c) {
+#pragma unroll
+    for (int q = 0; q < MT; ++q) {
+        float x = fmaxf(fmaxf(sc[q][0][0], sc[q][0][1]), sc[q][0][2]);
+        x = fmaxf(fmaxf(x, sc[q][0][3]), sc[q][1][0]);
+        x = fmaxf(fmaxf(x, sc[q][1][1]), sc[q][1][2]);
+        t[q] = fmaxf(x, sc[q][1][3]) * c;
+    }
+}
+
+// Softmax weights, in the lane and order of the second product's operand.
+// Their sum comes from the same rounded weights, as one more product, with ones.
+template <int D, int MT>
+__device__ __forceinline__ void weights(Sums<D, MT>& a, bf16x8_t (&pf)[MT], const f32x4_t (&sc)[MT][2], float c) {
+    const uint32_t one2 = 0x3F803F80u;
+    const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{one2, one2, one2, one2});
+#pragma unroll
+    for (int q = 0; q < MT; ++q) {
+        const float ref = a.m[q] == -INFINITY ? 0.f : a.m[q];
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_exp2f(fmaf(sc[q][j / 4][j % 4], c, -ref));
+        u32x4_t w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
+        pf[q] = __builtin_bit_cast(bf16x8_t, w);
+        a.l[q] = mfma(ones, pf[q], a.l[q]);
+    }
+}
+
+// The common tile, at src: every row sees every key.  False, with the sums
+// untouched, if a reference has to move.
+template <int FMT, int D, int MT>
+__device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const uint8_t* src, int lane,
+                                             const bf16x8_t (&qf)[MT][D / 32], float c) {
+    Raw<FMT, D> r;
+    read_keys<FMT, D>(r, src, lane);
+    f32x4_t sc[MT][2];
+    scores<FMT, D, MT>(sc, r, qf);
+    float top[MT];
+    tops<MT>(top, sc, c);
+    bool move = false;
+#pragma unroll
+    for (int q = 0; q < MT; ++q) move |= top[q] > sums.m[q] + kSlack;
+    if (__any(move)) return false;
+    read_values<FMT, D>(r, src, lane);
+    bf16x8_t pf[MT];
+    weights<D, MT>(sums, pf, sc, c);
+    each_v<FMT, D>(r, 0xFF, [&](int n, const bf16x8_t& v) {
+#pragma unroll
+        for (int q = 0; q < MT; ++q) sums.o[q][n] = mfma(v, pf[q], sums.o[q][n]);
+    });
+    return true;
+}
+
+// Any tile.  live: which of the lane group's 8 keys exist; kg: the first of
+// them.  WILD: some value is infinite or NaN.
+template <int FMT, int D, int MT, bool WILD>
+__device__ __forceinline__ void attend_part(Sums<D, MT>& a, const Raw<FMT, D>& r, const bf16x8_t (&qf)[MT][D / 32],
+                                            const View (&vw)[MT], int kg, uint32_t live, int sinks, float c) {
+    f32x4_t sc[MT][2];
+    scores<FMT, D, MT>(sc, r, qf);
+    uint32_t seen[MT];
+#pragma unroll
+    for (int q = 0; q < MT; ++q) {
+        seen[q] = low_bits(vw[q].up - kg) & (~low_bits(vw[q].lo - kg) | low_bits(sinks - kg)) & live;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (!((seen[q] >> j) & 1)) sc[q][j / 4][j % 4] = -INFINITY;
+    }
+    float tm[MT];
+    tops<MT>(tm, sc, c);
+#pragma unroll
+    for (int q = 0; q < MT; ++q) {
+        float t = fmaxf(tm[q], __shfl_xor(tm[q], 16));
+        t = fmaxf(t, __shfl_xor(t, 32));
+        if (!__any(t > a.m[q] + kSlack)) continue;
+        const float mn = fmaxf(a.m[q], t);
+        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(a.m[q] - mn);
+        a.m[q] = mn;
+        a.l[q] *= f;
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) a.o[q][n] *= f;
+    }
+    bf16x8_t pf[MT];
+    weights<D, MT>(a, pf, sc, c);
+    if constexpr (WILD) {
+        // One product would spread 0 x inf to rows that do not see the key.
+        // So a product per row, with the values that this row sees, of which
+        // only that row is kept.
+        for (int n = 0; n < 16; ++n) {
+            Raw<FMT, D> x = r;
+            decode_anew(x);
+#pragma unroll
+            for (int q = 0; q < MT; ++q) {
+                const uint32_t own = __shfl(seen[q], (threadIdx.x & 48) + n);
+                const bool mine = (threadIdx.x & 15) == (unsigned)n;
+                each_v<FMT, D>(x, own, [&](int k, const bf16x8_t& v) {
+                    const f32x4_t y = mfma(v, pf[q], f32x4_t{0.f, 0.f, 0.f, 0.f});
+                    if (mine) a.o[q][k] += y;
+                });
+            }
+        }
+    } else {
+        each_v<FMT, D>(r, live, [&](int k, const bf16x8_t& v) {
+#pragma unroll
+            for (int q = 0; q < MT; ++q) a.o[q][k] = mfma(v, pf[q], a.o[q][k]);
+        });
+    }
+}
+
+// How the work is divided.  kEven: a workgroup per sequence, head and set of
+// rows.  kQuota: all (sequence, head, set of rows) are laid end to end, a unit
+// per tile of keys, and every workgroup takes the same number of units, which
+// may begin and end inside one: such pieces leave float32 sums that k_attn_join
+// adds up.  The workgroups find their units themselves, by a prefix sum over
+// the sequences, since only the device knows the lengths.
+enum { kEven, kQuota };
+constexpr int kQuotaBatch = 1024;                  // sequences kQuota handles: four per thread, their sums in LDS
+constexpr int kQuotaLeast = 16;                    // units a workgroup takes at least, where a sequence has them
+
+// A sequence's sets of `per` rows, and the units each counts: as many tiles of
+// keys as any of the sets sees, and one at least, so that every row is
+// written.
+struct Units {
+    int tiles, sets;
+};
+__device__ __forceinline__ Units units_of(const AttnArgs& a, const Seq& sq, int per) {
+    const int rows = sq.n * a.G;
+    if (rows == 0) return Units{0, 0};
+    int64_t t = ((int64_t)sq.kv + kTile - 1) / kTile;
+    if (a.window > 0) {
+        // a set's rows are of at most (per - 1) / G + 2 tokens; an interval of
+        // keys touches (length + 2 (kTile - 1)) / kTile tiles at most
+        const int64_t len = (int64_t)a.window + (a.causal ? (min(per, rows) - 1) / a.G + 1 : sq.n);
+        t = min(t, (int64_t)((a.sinks + (int64_t)kTile - 1) / kTile + (len + 2 * (kTile - 1)) / kTile));
+    }
+    return Units{max((int)t, 1), (rows + per - 1) / per};
+}
+
+// A workgroup's 4 waves: WR along the rows (MT tiles of 16 each), 4 / WR along
+// the keys.  NB: tiles in a wave's ring.  WPE: waves per SIMD.
+template <int FMT, int D, int MT, int WR, int NB, int WPE, int MODE>
+__global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
+    constexpr int NT = D / 16, KS = D / 32, WK = kWaves / WR, ROWS = 16 * MT * WR;
+    constexpr int TPR = 16 / WR, E = D / TPR;      // threads per row and elements per thread in the join
+    constexpr bool ONCE = WR == 1;                 // each key is read by one wave only
+    using T = Tile<FMT, D>;
+    typedef float JoinRows[kWaves][16][D + 4];
+    constexpr int kRing = NB * T::kBytes, kLds = kWaves * kRing > (int)sizeof(JoinRows) ? kWaves * kRing : sizeof(JoinRows);
+    __shared__ __align__(1024) uint8_t lds[kLds];
+    __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
+    __shared__ int64_t sh_start[MODE == kQuota ? kQuotaBatch + 1 : 1];
+    __shared__ int64_t sh_sum[kWaves];
+    __shared__ int sh_top[kWaves];
+    JoinRows& sh_o = *reinterpret_cast<JoinRows*>(lds);
+    const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wr = wave % WR, wk = wave / WR;
+    const uint8_t* const base = lds + wave * kRing;
+    const uint32_t mine = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)(lds + wave * kRing));
+    const int m = lane % 16, g = lane / 16;
+    const ScalarInts cu_q = (ScalarInts)(uintptr_t)a.cu_q, kv_lens = (ScalarInts)(uintptr_t)a.kv_lens;
+
+    // this workgroup's units [unit, last)
+    int64_t unit, last;
+    if constexpr (MODE == kQuota) {
+        int64_t before[4], sum = 0;
+        int most = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int b = tid * 4 + i;
+            before[i] = sum;
+            if (b < a.B) {
+                const Units u = units_of(a, sequence(a, b, a.cu_q, a.kv_lens), ROWS);
+                sum += (int64_t)u.sets * u.tiles;
+                most = max(most, u.tiles);
+            }
+        }
+        int64_t incl = sum;
+#pragma unroll
+        for (int off = 1; off < kWave; off <<= 1) {
+            const int64_t o = __shfl_up(incl, off);
+            if (lane >= off) incl += o;
+            most = max(most, __shfl_xor(most, off));
+        }
+        if (lane == kWave - 1) {
+            sh_sum[wave] = incl;
+            sh_top[wave] = most;
+        }
+        __syncthreads();
+        int64_t all = 0, ahead = 0;
+        most = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) ahead += sh_sum[w];
+            all += sh_sum[w];
+            most = max(most, sh_top[w]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (tid * 4 + i <= a.B) sh_start[tid * 4 + i] = ahead + incl - sum + before[i];
+        if (tid == 0) sh_start[a.B] = all;
+        const int64_t share = (all * a.Hk + gridDim.x - 1) / gridDim.x;
+        const int64_t quota = max(share, (int64_t)min(most, kQuotaLeast));
+        unit = blockIdx.x * quota;
+        last = min(unit + quota, all * a.Hk);
+        __syncthreads();
+        if (blockIdx.x == 0) {                     // for the join
+            for (int b = tid; b <= a.B; b += kThreads) a.start[b] = sh_start[b];
+            if (tid == 0) a.start[a.B + 1] = quota;
+        }
+    } else {
+        unit = blockIdx.x;                         // set of rows, then by row_tiles
+        last = INT64_MAX;
+    }
+
+    while (unit < last) {
+        int b, hk, set, c0, c1;
+        bool complete;                             // all of its keys are taken here
+        if constexpr (MODE == kQuota) {
+            int lo = 0, hi = a.B;                  // the last sequence that starts at or before the unit
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sh_start[mid] * a.Hk <= unit) lo = mid; else hi = mid;
+            }
+            b = __builtin_amdgcn_readfirstlane(lo);
+        } else {
+            b = (int)(blockIdx.x / (unsigned)(a.row_tiles * a.Hk));
+        }
+        const Seq sq = sequence(a, b, cu_q, kv_lens);
+        const int rows = sq.n * a.G;               // (token, head of the group) pairs, token-major
+        if constexpr (MODE == kQuota) {
+            const Units u = units_of(a, sq, ROWS);
+            const int64_t in = unit - sh_start[b] * a.Hk, per = (int64_t)u.sets * u.tiles;
+            hk = __builtin_amdgcn_readfirstlane((int)(in / per));
+            const int64_t rest = in - hk * per;
+            set = __builtin_amdgcn_readfirstlane((int)(rest / u.tiles));
+            c0 = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)set * u.tiles));
+            c1 = (int)min((int64_t)u.tiles, c0 + (last - unit));
+            complete = c0 == 0 && c1 == u.tiles;
+            unit += c1 - c0;
+        } else {
+            const int in = (int)(blockIdx.x % (unsigned)(a.row_tiles * a.Hk));
+            hk = in / a.row_tiles;
+            set = in % a.row_tiles + (int)(unit - blockIdx.x);
+            if ((int64_t)set * ROWS >= rows) return;
+            c0 = 0;
+            c1 = INT32_MAX;
+            complete = true;
+            unit += a.row_tiles;
+        }
+        const int r0 = set * ROWS;
+        const ScalarInts trow = (ScalarInts)(uintptr_t)(a.table + (size_t)b * a.W);
         const int p0 = sq.kv - sq.n + r0 / a.G, p1 = sq.kv - sq.n + (min(r0 + ROWS, rows) - 1) / a.G;
         const Range rg = tiles_of(a, p0, p1, sq.kv);
-        const bool alone = rg.total <= a.share || a.nsplit == 1;
-        const int c0 = split * a.share;
-        if (split > 0 && (alone || c0 >= rg.total)) continue;
-        // the last workgroup along the keys takes what is left
-        const int c1 = alone || split == a.nsplit - 1 ? rg.total : min(c0 + a.share, rg.total);
+        c1 = complete ? rg.total : min(c1, rg.total);
+        const int rw = r0 + 16 * MT * wr;          // this wave's first row
 
         // queries and views of this lane's row in each 16-row tile
         bf16x8_t qf[MT][KS];
         View vw[MT];
 #pragma unroll
         for (int q = 0; q < MT; ++q) {
-            const int r = r0 + 16 * q + m;
+            const int r = rw + 16 * q + m;
             const bool in = r < rows;
             const int tok = in ? r / a.G : 0, h = in ? hk * a.G + r % a.G : 0;
             const int p = sq.kv - sq.n + tok;
@@ -300,220 +670,186 @@ __global__ __launch_bounds__(kThreads) void k_attn(AttnArgs a) {
                 qf[q][s] = __builtin_bit_cast(bf16x8_t, x);
             }
         }
-        // keys that every row of the tile sees: [all_lo, all_up) and below all_sink
+        // keys that every row of the tile sees: [all_lo, all_up) and below sinks
         const int all_up = p0 < 0 ? 0 : a.causal ? min(p0 + 1, sq.kv) : sq.kv;
         const int all_lo = a.window > 0 ? (int)max((int64_t)p1 - a.window + 1, (int64_t)0) : 0;
 
-        f32x4_t o[MT][NT];
-        float mx[MT], ls[MT];
+        Sums<D, MT> sums;
 #pragma unroll
         for (int q = 0; q < MT; ++q) {
-            mx[q] = -INFINITY;
-            ls[q] = 0.f;
+            sums.m[q] = -INFINITY;
+            sums.l[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) o[q][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int n = 0; n < NT; ++n) sums.o[q][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
 
-        Raw<FMT, D> cur, nxt;
-        Pages pc{}, pn{};
-        int c = c0 + wave;
+        // tiles c0 + wk, c0 + wk + WK, ...
         auto tile_at = [&](int x) { return x < rg.head ? x : rg.lo + x - rg.head; };
+        // A tile that every row sees whole needs no mask.  Else keys in no page
+        // or behind the last are dead (their values count as 0) and the others
+        // are masked row by row.
+        auto whole_at = [&](int key0, const Pages& p) {
+            return p.a >= 0 && p.b >= 0 && key0 + kTile <= all_up && (key0 >= all_lo || key0 + kTile <= a.sinks);
+        };
+        auto live_at = [&](int key0, const Pages& p) {
+            return p.of(g < 2) >= 0 ? low_bits(sq.kv - key0 - 8 * g) : 0u;
+        };
+        // A ring of NB tiles per wave in LDS, NB - 1 of them on their way while
+        // one is read.  The loop over common tiles (every row sees every key, no
+        // reference moves) has no other branch in it, so that the sums stay in
+        // their registers; anything else leaves it before the sums are touched.
+        // Loads past the end ask for the last tile again, so that the number
+        // under way is always the same.
+        bool wild = false;
+        int c = c0 + wk;
+        uint32_t at = 0;                           // tile c's slot
+        auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
+        auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
+        Pages pg0{}, pg1{}, pg2{}, pg3{};          // of tiles c, c + WK, ...
         if (c < c1) {
-            pc = pages_of(a, trow, tile_at(c), sq.kv);
-            load_tile<FMT, D>(cur, a, pc, tile_at(c), hk, lane);
+            pg0 = pages_for(c);
+            pg1 = pages_for(c + WK);
+            pg2 = pages_for(c + 2 * WK);
+            fetch<FMT, D, ONCE>(mine, a, pg0, tile_for(c), hk, lane);
+            fetch<FMT, D, ONCE>(mine + T::kBytes, a, pg1, tile_for(c + WK), hk, lane);
+            if constexpr (NB == 3) {
+                pg3 = pages_for(c + 3 * WK);
+                fetch<FMT, D, ONCE>(mine + 2 * T::kBytes, a, pg2, tile_for(c + 2 * WK), hk, lane);
+            }
         }
-        for (; c < c1; c += kWaves) {
-            const int tile = tile_at(c), key0 = tile * kTile;
-            if (c + kWaves < c1) {
-                const int tn = tile_at(c + kWaves);
-                pn = pages_of(a, trow, tn, sq.kv);
-                load_tile<FMT, D>(nxt, a, pn, tn, hk, lane);
+        // the queries are used here, so that the wait for them is not left to
+        // the loops below, where it would be for the tiles' loads too
+#pragma unroll
+        for (int q = 0; q < MT; ++q)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                u32x4_t x = __builtin_bit_cast(u32x4_t, qf[q][s]);
+                asm volatile("" : "+v"(x));
+                qf[q][s] = __builtin_bit_cast(bf16x8_t, x);
             }
-            // scores
-            f32x4_t sc[MT][2];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int q = 0; q < MT; ++q) sc[q][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const bf16x8_t kf = k_operand<FMT, D>(cur, t, s);
-#pragma unroll
-                    for (int q = 0; q < MT; ++q)
-                        sc[q][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[q][s], sc[q][t], 0, 0, 0);
-                }
-            }
-            // A tile that every row sees whole needs no mask.  Else: keys in
-            // no page or behind the last are dead (their values count as 0), the rest is
-            // masked row by row.
-            const bool whole = pc.p[0] >= 0 && pc.p[1] >= 0 && key0 + kTile <= all_up &&
-                               (key0 >= all_lo || key0 + kTile <= a.sinks);
-            uint32_t live = 0xFF;                  // of keys key0 + 8 g + j
-            uint32_t seen[MT];
-            bool slow = false;
-            if (!whole) {
-                const int kg = key0 + 8 * g;
-                const int left = (g < 2 ? pc.p[0] : pc.p[1]) >= 0 ? min(max(sq.kv - kg, 0), 8) : 0;
-                live = (1u << left) - 1;
-#pragma unroll
-                for (int q = 0; q < MT; ++q) {
-                    uint32_t see = 0;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        see |= (uint32_t)(kg + j < vw[q].up && (kg + j >= vw[q].lo || kg + j < a.sinks)) << j;
-                    seen[q] = see & live;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (!((seen[q] >> j) & 1)) sc[q][j / 4][j % 4] = -INFINITY;
-                }
-                slow = __any(wild_values<FMT, D>(cur, live));
-            }
-            // softmax weights, in the lane and order of the second product's operand
-            bf16x8_t pf[MT];
-            float pw[MT][8];
-            bool up = false;
-            float tm[MT];
-#pragma unroll
-            for (int q = 0; q < MT; ++q) {
-                tm[q] = sc[q][0][0];
-#pragma unroll
-                for (int j = 1; j < 8; ++j) tm[q] = fmaxf(tm[q], sc[q][j / 4][j % 4]);
-                tm[q] *= a.c;
-                up |= tm[q] > mx[q] + kSlack;
-            }
-            if (__any(up)) {
-#pragma unroll
-                for (int q = 0; q < MT; ++q) {
-                    float t = fmaxf(tm[q], __shfl_xor(tm[q], 16));
-                    t = fmaxf(t, __shfl_xor(t, 32));
-                    const float mn = fmaxf(mx[q], t);
-                    const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mx[q] - mn);
-                    mx[q] = mn;
-                    ls[q] *= f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) o[q][n] *= f;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < MT; ++q) {
-                const float ref = mx[q] == -INFINITY ? 0.f : mx[q];
-                u32x4_t w;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    pw[q][j] = __builtin_amdgcn_exp2f(fmaf(sc[q][j / 4][j % 4], a.c, -ref));
-                    ls[q] += pw[q][j];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = pack_bf16(pw[q][2 * i], pw[q][2 * i + 1]);
-                pf[q] = __builtin_bit_cast(bf16x8_t, w);
-            }
-            if (!slow) {
-                auto pv = [&](auto U) {
-                    constexpr int u = decltype(U)::value;
-                    bf16x8_t va, vb;
-                    v_operand<FMT, D, u>(cur, live, va, vb);
-#pragma unroll
-                    for (int q = 0; q < MT; ++q) {
-                        o[q][2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(va, pf[q], o[q][2 * u], 0, 0, 0);
-                        o[q][2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, pf[q], o[q][2 * u + 1], 0, 0, 0);
-                    }
-                };
-                pv(std::integral_constant<int, 0>{});
-                pv(std::integral_constant<int, 1>{});
-                if constexpr (D == 128) {
-                    pv(std::integral_constant<int, 2>{});
-                    pv(std::integral_constant<int, 3>{});
-                }
+        // tile c is done with: its slot takes the tile NB steps on
+        auto advance = [&] {
+            fetch<FMT, D, ONCE>(mine + at, a, NB == 3 ? pg3 : pg2, tile_for(c + NB * WK), hk, lane);
+            c += WK;
+            at = at == (NB - 1) * T::kBytes ? 0 : at + T::kBytes;
+            pg0 = pg1;
+            pg1 = pg2;
+            if constexpr (NB == 3) {
+                pg2 = pg3;
+                pg3 = pages_for(c + 3 * WK);
             } else {
-                // A partly visible tile with an infinite or NaN value: the
-                // matrix product would spread 0 x inf to rows that do not see
-                // it, so only the rows that see a key add it, one key at a time.
-                for (int gs = 0; gs < 4; ++gs) {
-                    const int64_t base = ((int64_t)max(pc.p[gs / 2], 0) * a.Hk + hk) << a.shift;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int row = (key0 + 8 * gs + j) & ((1 << a.shift) - 1);
-#pragma unroll
-                        for (int q = 0; q < MT; ++q) {
-                            const float w = __shfl(pw[q][j], m + 16 * gs);
-                            const bool sees = (__shfl(seen[q], m + 16 * gs) >> j) & 1;
-                            if (!__any(sees)) continue;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float x = value_at<FMT, D>(a, base, row, (4 * g + i) * NT + n);
-                                    if (sees) o[q][n][i] = fmaf(w, x, o[q][n][i]);
-                                }
-                        }
-                    }
-                }
+                pg2 = pages_for(c + 2 * WK);
             }
-            cur = nxt;
-            pc = pn;
+        };
+        constexpr int kUnder = (NB - 1) * T::kFetches;
+        while (c < c1) {
+            while (c < c1 && whole_at(tile_at(c) * kTile, pg0)) {
+                wait_loads<kUnder>();
+                if (!attend_whole<FMT, D, MT>(sums, base + at, lane, qf, a.c)) break;
+                advance();
+            }
+            if (c >= c1) break;
+            // any tile
+            wait_loads<kUnder>();
+            const int key0 = tile_at(c) * kTile;
+            Raw<FMT, D> r;
+            read_keys<FMT, D>(r, base + at, lane);
+            read_values<FMT, D>(r, base + at, lane);
+            const uint32_t live = live_at(key0, pg0);
+            if (!whole_at(key0, pg0) && __any(wild_values<FMT, D>(r, live))) wild = true;
+            else attend_part<FMT, D, MT, false>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+            advance();
         }
+        // tiles put off: those that rows see in part and that hold an infinite
+        // or NaN value.  Rare, and kept out of the loop above so that it costs
+        // that loop no registers.
+        if (wild) {
+            for (c = c0 + wk; c < c1; c += WK) {
+                const int key0 = tile_at(c) * kTile;
+                const Pages pc = pages_for(c);
+                if (whole_at(key0, pc)) continue;
+                wait_loads<0>();
+                fetch<FMT, D, ONCE>(mine, a, pc, tile_at(c), hk, lane);
+                wait_loads<0>();
+                Raw<FMT, D> r;
+                read_keys<FMT, D>(r, base, lane);
+                read_values<FMT, D>(r, base, lane);
+                const uint32_t live = live_at(key0, pc);
+                if (__any(wild_values<FMT, D>(r, live)))
+                    attend_part<FMT, D, MT, true>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+            }
+        }
+        wait_loads<0>();                           // the ring's memory is used again below
 
-        // join the four waves, 16 rows at a time; a thread takes D/16
-        // elements of one row
+        // join the waves along the keys, 16 rows of each row wave at a time
 #pragma unroll
         for (int q = 0; q < MT; ++q) {
-            float l = ls[q] + __shfl_xor(ls[q], 16);
-            l += __shfl_xor(l, 32);
             __syncthreads();
             if (g == 0) {
-                sh_m[wave][m] = mx[q];
-                sh_l[wave][m] = l;
+                sh_m[wave][m] = sums.m[q];
+                sh_l[wave][m] = sums.l[q][0];
             }
+            float* row = sh_o[wave][m];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int n = 0; n < NT; n += 4)
-                    *reinterpret_cast<f32x4_t*>(&sh_o[wave][m][(4 * g + i) * NT + n]) =
-                        f32x4_t{o[q][n][i], o[q][n + 1][i], o[q][n + 2][i], o[q][n + 3][i]};
+                    *reinterpret_cast<f32x4_t*>(row + (4 * g + i) * NT + n) =
+                        f32x4_t{sums.o[q][n][i], sums.o[q][n + 1][i], sums.o[q][n + 2][i], sums.o[q][n + 3][i]};
             __syncthreads();
-            const int rr = tid / 16, d0 = (tid % 16) * NT;
-            const int r = r0 + 16 * q + rr;
+            const int wj = tid / TPR / 16, rr = tid / TPR % 16, d0 = tid % TPR * E;
+            const int r = r0 + 16 * MT * wj + 16 * q + rr;
             if (r < rows) {
-                float top = sh_m[0][rr];
+                float top = sh_m[wj][rr];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh_m[w][rr]);
+                for (int w = 1; w < WK; ++w) top = fmaxf(top, sh_m[wj + w * WR][rr]);
                 const float ref = top == -INFINITY ? 0.f : top;
-                float acc[NT], lt = 0.f;
+                float acc[E], lt = 0.f;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n] = 0.f;
+                for (int n = 0; n < E; ++n) acc[n] = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    const float f = __builtin_amdgcn_exp2f(sh_m[w][rr] - ref);
-                    lt += f * sh_l[w][rr];
+                for (int w = 0; w < WK; ++w) {
+                    const float f = __builtin_amdgcn_exp2f(sh_m[wj + w * WR][rr] - ref);
+                    const float* part = sh_o[wj + w * WR][rr] + d0;
+                    lt += f * sh_l[wj + w * WR][rr];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[n] += f * sh_o[w][rr][d0 + n];
+                    for (int n = 0; n < E; ++n) acc[n] += f * part[n];
                 }
                 const int t = sq.start + r / a.G, h = hk * a.G + r % a.G;
-                if (alone) {
+                if (complete) {
                     const float inv = lt == 0.f ? 0.f : 1.f / lt;
-                    uint32_t w[NT / 2];
-#pragma unroll
-                    for (int n = 0; n < NT / 2; ++n) w[n] = pack_bf16(acc[2 * n] * inv, acc[2 * n + 1] * inv);
                     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + (int64_t)t * a.os + (int64_t)h * D + d0);
-                    if constexpr (NT == 8) *reinterpret_cast<u32x4_t*>(dst) = u32x4_t{w[0], w[1], w[2], w[3]};
-                    else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-                } else {
-                    const int64_t at = ((int64_t)t * a.H + h) * a.nsplit + split;
+                    if constexpr (E == 4) {
+                        *reinterpret_cast<uint2*>(dst) =
+                            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+                    } else {
 #pragma unroll
-                    for (int n = 0; n < NT; n += 4)
+                        for (int n = 0; n < E; n += 8)
+                            *reinterpret_cast<u32x4_t*>(dst + n / 2) =
+                                u32x4_t{pack_bf16(acc[n] * inv, acc[n + 1] * inv), pack_bf16(acc[n + 2] * inv, acc[n + 3] * inv),
+                                        pack_bf16(acc[n + 4] * inv, acc[n + 5] * inv),
+                                        pack_bf16(acc[n + 6] * inv, acc[n + 7] * inv)};
+                    }
+                } else {
+                    // a piece that begins inside its units is the workgroup's
+                    // first, one that begins with them and ends early its last
+                    const int64_t at = ((int64_t)blockIdx.x * 2 + (c0 == 0)) * ROWS + (r - r0);
+#pragma unroll
+                    for (int n = 0; n < E; n += 4)
                         *reinterpret_cast<f32x4_t*>(a.part + at * D + d0 + n) =
                             f32x4_t{acc[n], acc[n + 1], acc[n + 2], acc[n + 3]};
                     if (d0 == 0) *reinterpret_cast<float2*>(a.stat + at * 2) = make_float2(top, lt);
                 }
             }
         }
+        __syncthreads();                           // the next rows' tiles come where the join was read
     }
 }
 
-// Rows whose keys several workgroups shared: out = sum 2^(m_s - m) O_s / sum
-// 2^(m_s - m) l_s over the shares in order.  A wave per row.
+// Rows whose units several workgroups shared: out = sum 2^(m_s - m) O_s / sum
+// 2^(m_s - m) l_s over the pieces in order.  A wave per row.
 template <int D>
-__device__ __forceinline__ void join_row(const AttnArgs& a, int rows_per_tile, int64_t row, int lane) {
+__device__ __forceinline__ void join_row(const AttnArgs& a, int per, int64_t row, int lane) {
     constexpr int E = D / 64;                      // elements per lane
     const int t = (int)(row / a.H), h = (int)(row % a.H);
     // the sequence of row t: the last that starts at or before it
@@ -522,26 +858,32 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int rows_per_tile, i
         const int mid = (lo + hi) >> 1;
         if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
     }
-    const Seq sq = sequence(a, lo);
+    const Seq sq = sequence(a, lo, a.cu_q, a.kv_lens);
     if (t < sq.start || t >= sq.start + sq.n) return;
-    const int rows = sq.n * a.G, r = (t - sq.start) * a.G + h % a.G;
-    const int r0 = r / rows_per_tile * rows_per_tile;
-    const Range rg = tiles_of(a, sq.kv - sq.n + r0 / a.G, sq.kv - sq.n + (min(r0 + rows_per_tile, rows) - 1) / a.G, sq.kv);
-    if (rg.total <= a.share) return;               // written by its one workgroup
-    const int used = min((rg.total + a.share - 1) / a.share, a.nsplit);
-    const float* stat = a.stat + row * a.nsplit * 2;
+    const int r = (t - sq.start) * a.G + h % a.G, set = r / per;
+    const Units u = units_of(a, sq, per);
+    const int64_t quota = a.start[a.B + 1];
+    const int64_t first = a.start[lo] * a.Hk + ((int64_t)(h / a.G) * u.sets + set) * u.tiles;
+    const int w0 = (int)(first / quota), w1 = (int)((first + u.tiles - 1) / quota);
+    if (w0 == w1) return;                          // written by its one workgroup
+    // pieces: of w0 from `first` on (its last unless it begins there with its
+    // units), then of each workgroup to w1 its first
+    auto piece = [&](int w) { return ((int64_t)w * 2 + (w * quota <= first)) * per + (r - set * per); };
+    const int used = w1 - w0 + 1;
     float top = -INFINITY;
-    for (int s = lane; s < used; s += kWave) top = fmaxf(top, stat[2 * s]);
+    for (int s = lane; s < used; s += kWave) top = fmaxf(top, a.stat[piece(w0 + s) * 2]);
 #pragma unroll
     for (int off = kWave / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
     const float ref = top == -INFINITY ? 0.f : top;
-    const float* part = a.part + row * a.nsplit * D + lane * E;
     float acc[E] = {}, l = 0.f;
-    for (int s = 0; s < used; ++s) {
-        const float f = __builtin_amdgcn_exp2f(stat[2 * s] - ref);
-        l += f * stat[2 * s + 1];
+#pragma unroll 8
+    for (int s = 0; s < used; ++s) {               // unrolled, so that eight loads are under way
+        const int64_t at = piece(w0 + s);
+        const float2 ml = *reinterpret_cast<const float2*>(a.stat + at * 2);
+        const float f = __builtin_amdgcn_exp2f(ml.x - ref);
+        l += f * ml.y;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * part[(int64_t)s * D + e];
+        for (int e = 0; e < E; ++e) acc[e] += f * a.part[at * D + lane * E + e];
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* dst = a.out + (int64_t)t * a.os + (int64_t)h * D + lane * E;
@@ -550,73 +892,87 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int rows_per_tile, i
 }
 
 template <int D>
-__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a, int rows_per_tile) {
+__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a, int per) {
     const int lane = threadIdx.x % kWave;
     for (int64_t row = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave; row < (int64_t)a.T * a.H;
          row += (int64_t)gridDim.x * kWaves)
-        join_row<D>(a, rows_per_tile, row, lane);
+        join_row<D>(a, per, row, lane);
 }
 
 // Launch shape: a function of the sizes alone, so that the workspace's size
 // and the launch agree.
 struct Shape {
-    int mt, row_tiles, share, nsplit;
+    int mode, mt, wr, row_tiles, grid;
 };
 Shape shape_of(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c) {
     Shape s{};
+    const bool fp4 = c.format == MOE_KV_MXFP4, wide = !fp4 && c.head_dim == 128;
     const int64_t G = p.heads / c.kv_heads;
     const int64_t mq = p.max_q < p.num_tokens ? p.max_q : p.num_tokens;
     const int64_t rows = mq * G;
-    s.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    int64_t tiles = (rows + 16 * s.mt - 1) / (16 * s.mt);
+    s.mt = rows <= 16 || wide ? 1 : 2;
+    const int64_t sets = (rows + 16 * s.mt - 1) / (16 * s.mt);
+    s.wr = sets <= 1 ? 1 : sets <= 2 ? 2 : 4;
+    const int64_t per = 16 * s.mt * s.wr;
+    int64_t tiles = (rows + per - 1) / per;
     int64_t keys = p.max_kv;
     if (p.window > 0) {
-        const int64_t w = (int64_t)p.window + 16 * s.mt / G + 1 + p.sinks + 2 * kTile;
+        const int64_t w = (int64_t)p.window + per / G + 1 + p.sinks + 2 * kTile;
         if (w < keys) keys = w;
     }
-    const int64_t kt = (keys + kTile - 1) / kTile;
     const int64_t pairs = (int64_t)p.batch * c.kv_heads;
-    // the grid stays below 2^22 workgroups: more row tiles than fit are walked by a loop
+    // quotas where sequences are long enough to be divided and few sets of
+    // rows share their keys
+    if (p.batch <= kQuotaBatch && rows <= 2 * per && (keys + kTile - 1) / kTile > kQuotaLeast) {
+        s.mode = kQuota;
+        s.grid = 256 * (wide ? 1 : s.mt == 1 && fp4 ? 3 : 2);           // what the GPU holds at once
+        return s;
+    }
+    s.mode = kEven;
+    // the grid stays below 2^22 workgroups: more sets of rows than fit are walked by a loop
     const int64_t most = (1 << 22) / pairs > 0 ? (1 << 22) / pairs : 1;
-    if (tiles > most) tiles = most;
-    const int64_t want = 1024, base = pairs * tiles;
-    int64_t n = want / base;
-    const int64_t cap = kt / (2 * kWaves);         // two tiles a wave at least
-    if (n > cap) n = cap;
-    if (n > 64) n = 64;
-    if (n < 1) n = 1;
-    int64_t share = (kt + n - 1) / n;
-    share = (share + kWaves - 1) / kWaves * kWaves;
-    n = (kt + share - 1) / share;
-    s.row_tiles = (int)tiles;
-    s.share = (int)share;
-    s.nsplit = (int)n;
+    s.row_tiles = (int)(tiles < most ? tiles : most);
+    s.grid = (int)(pairs * s.row_tiles);
     return s;
+}
+
+template <int FMT, int D, int MODE>
+void launch_mode(const AttnArgs& a, const Shape& sh, hipStream_t s) {
+    // waves per SIMD: what the registers of MT tiles leave
+    constexpr bool fp4 = FMT == MOE_KV_MXFP4;
+    constexpr int MT = !fp4 && D == 128 ? 1 : 2, W1 = !fp4 ? 2 : D == 128 ? 3 : 4, W2 = !fp4 || D == 128 ? 2 : 3;
+    constexpr int N1 = 2, N2 = fp4 ? 3 : 2;
+    const dim3 grid(sh.grid), block(kThreads);
+    if (sh.mt == 1 && sh.wr == 1) hipLaunchKernelGGL((k_attn<FMT, D, 1, 1, N1, W1, MODE>), grid, block, 0, s, a);
+    else if (sh.wr == 1) hipLaunchKernelGGL((k_attn<FMT, D, MT, 1, N2, W2, MODE>), grid, block, 0, s, a);
+    else if (sh.wr == 2) hipLaunchKernelGGL((k_attn<FMT, D, MT, 2, N2, W2, MODE>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_attn<FMT, D, MT, 4, N2, W2, MODE>), grid, block, 0, s, a);
 }
 
 template <int FMT, int D>
 hipError_t launch_fmt(const AttnArgs& a, const Shape& sh, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.B * a.Hk * sh.nsplit * sh.row_tiles)), block(kThreads);
-    if (sh.mt == 1) hipLaunchKernelGGL((k_attn<FMT, D, 1>), grid, block, 0, s, a);
-    else if (sh.mt == 2) hipLaunchKernelGGL((k_attn<FMT, D, 2>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_attn<FMT, D, 4>), grid, block, 0, s, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || sh.nsplit == 1) return e;
+    if (sh.mode == kEven) {
+        launch_mode<FMT, D, kEven>(a, sh, s);
+        return hipGetLastError();
+    }
+    launch_mode<FMT, D, kQuota>(a, sh, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const int64_t wgs = ((int64_t)a.T * a.H + kWaves - 1) / kWaves;
-    hipLaunchKernelGGL((k_attn_join<D>), dim3((unsigned)(wgs < 65536 ? wgs : 65536)), block, 0, s, a, 16 * sh.mt);
+    hipLaunchKernelGGL((k_attn_join<D>), dim3((unsigned)(wgs < 65536 ? wgs : 65536)), dim3(kThreads), 0, s, a,
+                       16 * sh.mt * sh.wr);
     return hipGetLastError();
 }
 
-size_t sums_bytes(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c, const Shape& s) {
-    return (size_t)p.num_tokens * p.heads * s.nsplit * c.head_dim * sizeof(float);
-}
+// Pieces of a quota launch: rows of sums, two pieces a workgroup.
+int64_t piece_rows(const Shape& s) { return (int64_t)s.grid * 2 * 16 * s.mt * s.wr; }
 
 }  // namespace
 
 size_t attention_workspace_bytes(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c) {
     const Shape s = shape_of(p, c);
-    if (s.nsplit == 1) return 0;
-    return sums_bytes(p, c, s) + (size_t)p.num_tokens * p.heads * s.nsplit * 2 * sizeof(float);
+    if (s.mode == kEven) return 0;
+    return piece_rows(s) * (c.head_dim + 2) * sizeof(float) + ((size_t)p.batch + 2) * sizeof(int64_t);
 }
 
 hipError_t launch_attention(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c, void* workspace,
@@ -627,13 +983,16 @@ hipError_t launch_attention(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cac
     a.table = p.block_table; a.cu_q = p.cu_q; a.kv_lens = p.kv_lens;
     a.k = static_cast<const uint8_t*>(c.k); a.v = static_cast<const uint8_t*>(c.v);
     a.ks = c.k_scale; a.vs = c.v_scale;
-    a.part = static_cast<float*>(workspace);
-    a.stat = sh.nsplit > 1 ? a.part + sums_bytes(p, c, sh) / sizeof(float) : nullptr;
+    if (sh.mode == kQuota) {
+        a.part = static_cast<float*>(workspace);
+        a.stat = a.part + piece_rows(sh) * c.head_dim;
+        a.start = reinterpret_cast<int64_t*>(a.stat + piece_rows(sh) * 2);
+    }
     a.qs = p.q_stride; a.os = p.out_stride;
     a.B = p.batch; a.T = p.num_tokens; a.H = p.heads; a.Hk = c.kv_heads; a.G = p.heads / c.kv_heads;
     a.W = p.max_blocks; a.shift = log2_of(c.page_size); a.num_pages = c.num_pages;
     a.causal = p.causal != 0; a.window = p.window; a.sinks = p.sinks;
-    a.share = sh.share; a.nsplit = sh.nsplit; a.row_tiles = sh.row_tiles;
+    a.row_tiles = sh.row_tiles;
     a.c = p.scale * 1.4426950408889634f;
     if (c.format == MOE_KV_MXFP4)
         return c.head_dim == 128 ? launch_fmt<MOE_KV_MXFP4, 128>(a, sh, s) : launch_fmt<MOE_KV_MXFP4, 64>(a, sh, s);
