@@ -132,6 +132,8 @@ __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* src) {
             const u32x4_t x = *reinterpret_cast<const u32x4_t*>(src + 4 * i);
             dst[i] = x[0]; dst[i + 1] = x[1]; dst[i + 2] = x[2]; dst[i + 3] = x[3];
         }
+    } else if constexpr (N == 1) {
+        dst[0] = *reinterpret_cast<const uint32_t*>(src);
     } else {
         static_assert(N == 2, "");
         const uint2 x = *reinterpret_cast<const uint2*>(src);
@@ -139,24 +141,17 @@ __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* src) {
     }
 }
 
-// Pages of a tile's two halves of 16 keys; -1: outside the cache or behind the
-// last key.
+// Block table entries of a tile's two halves of 16 keys, as they stand.  They
+// are read through the scalar cache, and looked at only where they are used,
+// a tile or more later, so that nothing waits for them.
 struct Pages {
     int a, b;
-    __device__ __forceinline__ int of(bool first) const {
-        const int x = a, y = b;                    // values: a choice between the members would keep them in memory
-        return first ? x : y;
-    }
 };
-// The table is read through the scalar cache: vector loads return in order,
-// so a page looked up that way would wait for the tiles asked for before it.
 __device__ __forceinline__ Pages pages_of(const AttnArgs& a, ScalarInts row, int tile, int kv) {
-    auto look = [&](int key) {
-        const int p = row[min(key, kv - 1) >> a.shift];                 // kv <= W pages
-        return key < kv && (unsigned)p < (unsigned)a.num_pages ? p : -1;
-    };
-    return Pages{look(tile * kTile), look(tile * kTile + 16)};
+    const int key = tile * kTile;                  // below kv, which is within max_blocks pages
+    return Pages{row[key >> a.shift], row[min(key + 16, kv - 1) >> a.shift]};
 }
+__device__ __forceinline__ bool in_cache(const AttnArgs& a, int page) { return (unsigned)page < (unsigned)a.num_pages; }
 
 // 16 (or 4) bytes per lane from base + off (base the same for all lanes)
 // straight into LDS: lane L's go to lds + 16 L (4 L).  These loads write no
@@ -190,8 +185,8 @@ __device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pag
     const int mask = (1 << a.shift) - 1;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     // first row of each half; page 0 stands in for none: read, then not used
-    const int64_t b0 = (((int64_t)max(pg.a, 0) * a.Hk + hk) << a.shift) + ((tile * kTile) & mask);
-    const int64_t b1 = (((int64_t)max(pg.b, 0) * a.Hk + hk) << a.shift) + ((tile * kTile + 16) & mask);
+    const int64_t b0 = (((int64_t)(in_cache(a, pg.a) ? pg.a : 0) * a.Hk + hk) << a.shift) + ((tile * kTile) & mask);
+    const int64_t b1 = (((int64_t)(in_cache(a, pg.b) ? pg.b : 0) * a.Hk + hk) << a.shift) + ((tile * kTile + 16) & mask);
     if constexpr (FMT == MOE_KV_MXFP4 && D == 128) {
         // chunk c of row r is stored at c ^ (r / 8)
 #pragma unroll
@@ -376,15 +371,16 @@ __device__ __forceinline__ void each_v(const Raw<FMT, D>& r, uint32_t live, F f)
     }
 }
 
-template <int FMT, int D, int MT>
-__device__ __forceinline__ void scores(f32x4_t (&sc)[MT][2], const Raw<FMT, D>& r, const bf16x8_t (&qf)[MT][D / 32]) {
+// S^T of a tile; key(t, s): the operand of half tile t, step s.
+template <int D, int MT, typename Key>
+__device__ __forceinline__ void scores(f32x4_t (&sc)[MT][2], Key key, const bf16x8_t (&qf)[MT][D / 32]) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
         for (int q = 0; q < MT; ++q) sc[q][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < D / 32; ++s) {
-            const bf16x8_t kf = k_operand<FMT, D>(r, t, s);
+            const bf16x8_t kf = key(t, s);
 #pragma unroll
             for (int q = 0; q < MT; ++q) sc[q][t] = mfma(kf, qf[q][s], sc[q][t]);
         }
@@ -423,25 +419,65 @@ __device__ __forceinline__ void weights(Sums<D, MT>& a, bf16x8_t (&pf)[MT], cons
     }
 }
 
-// The common tile, at src: every row sees every key.  False, with the sums
-// untouched, if a reference has to move.
-template <int FMT, int D, int MT>
-__device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const uint8_t* src, int lane,
-                                             const bf16x8_t (&qf)[MT][D / 32], float c) {
+// A tile as the waves along the keys hold it: in registers as stored, decoded
+// on use.
+template <int FMT, int D> struct RawTile {
     Raw<FMT, D> r;
-    read_keys<FMT, D>(r, src, lane);
+    __device__ __forceinline__ RawTile(const uint8_t* src, int lane) {
+        read_keys<FMT, D>(r, src, lane);
+        read_values<FMT, D>(r, src, lane);
+    }
+    __device__ __forceinline__ bf16x8_t key(int t, int s) const { return k_operand<FMT, D>(r, t, s); }
+    // f(n, operand of tile n), of the keys in `keep`
+    template <typename F> __device__ __forceinline__ void values(uint32_t keep, F f) const { each_v<FMT, D>(r, keep, f); }
+    __device__ __forceinline__ bool wild(uint32_t live) const { return wild_values<FMT, D>(r, live); }
+    __device__ __forceinline__ void anew() { decode_anew(r); }
+};
+
+// A tile as the waves along the rows share it: operands in LDS, 16 bytes per
+// lane, dead keys' values already 0.
+template <int D> struct SharedTile {
+    const uint8_t* f;                              // + 16 lane
+    static constexpr int kBytes = (2 * (D / 32) + D / 16) * 1024;
+    __device__ __forceinline__ bf16x8_t at(int i) const { return *reinterpret_cast<const bf16x8_t*>(f + i * 1024); }
+    __device__ __forceinline__ bf16x8_t key(int t, int s) const { return at(t * (D / 32) + s); }
+    template <typename F> __device__ __forceinline__ void values(uint32_t keep, F f) const {
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+            u32x4_t w = __builtin_bit_cast(u32x4_t, at(2 * (D / 32) + n));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] &= ((keep >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((keep >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
+            f(n, __builtin_bit_cast(bf16x8_t, w));
+        }
+    }
+    __device__ __forceinline__ bool wild(uint32_t) const {
+        bool x = false;
+        for (int n = 0; n < D / 16; ++n) {
+            const u32x4_t w = __builtin_bit_cast(u32x4_t, at(2 * (D / 32) + n));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+        }
+        return x;
+    }
+    __device__ __forceinline__ void anew() {}
+};
+
+// The common tile: every row sees every key.  False, with the sums untouched,
+// if a reference has to move.
+template <int D, int MT, typename Src>
+__device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const Src& src, const bf16x8_t (&qf)[MT][D / 32], float c) {
     f32x4_t sc[MT][2];
-    scores<FMT, D, MT>(sc, r, qf);
+    scores<D, MT>(sc, [&](int t, int s) { return src.key(t, s); }, qf);
     float top[MT];
     tops<MT>(top, sc, c);
     bool move = false;
 #pragma unroll
     for (int q = 0; q < MT; ++q) move |= top[q] > sums.m[q] + kSlack;
     if (__any(move)) return false;
-    read_values<FMT, D>(r, src, lane);
     bf16x8_t pf[MT];
     weights<D, MT>(sums, pf, sc, c);
-    each_v<FMT, D>(r, 0xFF, [&](int n, const bf16x8_t& v) {
+    src.values(0xFF, [&](int n, const bf16x8_t& v) {
 #pragma unroll
         for (int q = 0; q < MT; ++q) sums.o[q][n] = mfma(v, pf[q], sums.o[q][n]);
     });
@@ -450,11 +486,11 @@ __device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const uint8_t* s
 
 // Any tile.  live: which of the lane group's 8 keys exist; kg: the first of
 // them.  WILD: some value is infinite or NaN.
-template <int FMT, int D, int MT, bool WILD>
-__device__ __forceinline__ void attend_part(Sums<D, MT>& a, const Raw<FMT, D>& r, const bf16x8_t (&qf)[MT][D / 32],
+template <int D, int MT, bool WILD, typename Src>
+__device__ __forceinline__ void attend_part(Sums<D, MT>& a, const Src& src, const bf16x8_t (&qf)[MT][D / 32],
                                             const View (&vw)[MT], int kg, uint32_t live, int sinks, float c) {
     f32x4_t sc[MT][2];
-    scores<FMT, D, MT>(sc, r, qf);
+    scores<D, MT>(sc, [&](int t, int s) { return src.key(t, s); }, qf);
     uint32_t seen[MT];
 #pragma unroll
     for (int q = 0; q < MT; ++q) {
@@ -484,24 +520,113 @@ __device__ __forceinline__ void attend_part(Sums<D, MT>& a, const Raw<FMT, D>& r
         // So a product per row, with the values that this row sees, of which
         // only that row is kept.
         for (int n = 0; n < 16; ++n) {
-            Raw<FMT, D> x = r;
-            decode_anew(x);
+            Src x = src;
+            x.anew();
 #pragma unroll
             for (int q = 0; q < MT; ++q) {
                 const uint32_t own = __shfl(seen[q], (threadIdx.x & 48) + n);
                 const bool mine = (threadIdx.x & 15) == (unsigned)n;
-                each_v<FMT, D>(x, own, [&](int k, const bf16x8_t& v) {
+                x.values(own, [&](int k, const bf16x8_t& v) {
                     const f32x4_t y = mfma(v, pf[q], f32x4_t{0.f, 0.f, 0.f, 0.f});
                     if (mine) a.o[q][k] += y;
                 });
             }
         }
     } else {
-        each_v<FMT, D>(r, live, [&](int k, const bf16x8_t& v) {
+        src.values(live, [&](int k, const bf16x8_t& v) {
 #pragma unroll
             for (int q = 0; q < MT; ++q) a.o[q][k] = mfma(v, pf[q], a.o[q][k]);
         });
     }
+}
+
+// A share of a tile on its way from memory to operands in LDS: waves 0 and 1
+// take the keys of a half tile each, 2 and 3 half of the values' elements.
+template <int FMT, int D> struct Staged {
+    static constexpr bool kFp4 = FMT == MOE_KV_MXFP4;
+    static constexpr int KW = kFp4 ? D / 32 : D / 8;                    // words of a lane's key
+    static constexpr int VW = kFp4 ? D / 16 : 8 * (D / 64);             // and of its values
+    uint32_t w[KW > VW ? KW : VW];
+    uint32_t sb[2];                                // scale bytes
+    __device__ __forceinline__ void load(const AttnArgs& a, const Pages& pg, int tile, int hk, int wave, int lane) {
+        const int m = lane % 16, g = lane / 16, mask = (1 << a.shift) - 1;
+        const int pa = in_cache(a, pg.a) ? pg.a : 0, pb = in_cache(a, pg.b) ? pg.b : 0;
+        if (wave < 2) {
+            const int64_t base = ((int64_t)(m < 8 ? pa : pb) * a.Hk + hk) << a.shift;
+            const int64_t row = base + ((tile * kTile + 8 * (m / 4) + 4 * wave + m % 4) & mask);
+            if constexpr (kFp4) {
+                load_words<KW>(w, a.k + row * (D / 2) + g * (D / 8));
+                sb[0] = a.ks[row * (D / 32) + g * D / 128];
+            } else {
+                load_words<KW>(w, a.k + (row * D + g * (D / 4)) * 2);
+            }
+        } else {
+            const int64_t base = ((int64_t)(g < 2 ? pa : pb) * a.Hk + hk) << a.shift;
+            const int row = (tile * kTile + 8 * g) & mask;
+            if constexpr (kFp4) {
+                constexpr int KG = v_keys_per_piece(D);
+#pragma unroll
+                for (int i = 0; i < 8 / KG; ++i)
+                    load_words<4>(w + 4 * i, a.v + base * (D / 2) + (row / KG + i) * (KG * D / 2) + m * 16);
+                const uint2 b = *reinterpret_cast<const uint2*>(a.vs + base * (D / 32) + row * (D / 32) + (m * D / 512) * 8);
+                sb[0] = b.x; sb[1] = b.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    load_words<D / 64>(w + j * (D / 64), a.v + ((base + row + j) * D + m * (D / 16) + (wave - 2) * (D / 32)) * 2);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* dst, const AttnArgs& a, const Pages& pg, int tile, int kv, int wave, int lane) {
+        const int g = lane / 16;
+        if (wave < 2) {
+            uint8_t* to = dst + wave * (D / 32) * 1024 + lane * 16;
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) {
+                if constexpr (kFp4)
+                    *reinterpret_cast<bf16x8_t*>(to + s * 1024) = decode8_bf16(w[s], e8m0_as_scale(sb[0]));
+                else
+                    *reinterpret_cast<u32x4_t*>(to + s * 1024) = u32x4_t{w[4 * s], w[4 * s + 1], w[4 * s + 2], w[4 * s + 3]};
+            }
+            return;
+        }
+        const int key0 = tile * kTile;
+        const bool ok0 = in_cache(a, pg.a), ok1 = in_cache(a, pg.b);
+        const uint32_t live = (g < 2 ? ok0 : ok1) ? low_bits(kv - key0 - 8 * g) : 0u;
+        uint8_t* to = dst + 2 * (D / 32) * 1024 + lane * 16;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const int u = (wave - 2) * (D / 64) + i;                    // this wave's pairs of elements
+            uint32_t x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (kFp4) {
+                    const uint32_t b = sb[j / 4];
+                    const float sc = __uint_as_float(j % 4 == 3 ? b >> 1 : b << (23 - 8 * (j % 4)));
+                    // the pair's byte of key j, brought down: which one depends on the wave
+                    const int at = j * (D / 32);
+                    x[j] = decode2<0>(w[at / 4] >> (8 * (at % 4) + 8 * u), sc);
+                } else {
+                    x[j] = w[j * (D / 64) + i];
+                }
+                x[j] = (live >> j) & 1 ? x[j] : 0;
+            }
+            u32x4_t lo, hi;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                lo[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x05040100u);
+                hi[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x07060302u);
+            }
+            *reinterpret_cast<u32x4_t*>(to + (2 * u) * 1024) = lo;
+            *reinterpret_cast<u32x4_t*>(to + (2 * u + 1) * 1024) = hi;
+        }
+    }
+};
+
+// A workgroup barrier that waits for this wave's LDS operations only: loads
+// from memory stay under way.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // How the work is divided.  kEven: a workgroup per sequence, head and set of
@@ -534,15 +659,17 @@ __device__ __forceinline__ Units units_of(const AttnArgs& a, const Seq& sq, int 
 }
 
 // A workgroup's 4 waves: WR along the rows (MT tiles of 16 each), 4 / WR along
-// the keys.  NB: tiles in a wave's ring.  WPE: waves per SIMD.
-template <int FMT, int D, int MT, int WR, int NB, int WPE, int MODE>
+// the keys.  WPE: waves per SIMD.
+template <int FMT, int D, int MT, int WR, int WPE, int MODE>
 __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
     constexpr int NT = D / 16, KS = D / 32, WK = kWaves / WR, ROWS = 16 * MT * WR;
     constexpr int TPR = 16 / WR, E = D / TPR;      // threads per row and elements per thread in the join
     constexpr bool ONCE = WR == 1;                 // each key is read by one wave only
+    constexpr bool SHARED = WR == kWaves;          // or by all four, at the same time
     using T = Tile<FMT, D>;
     typedef float JoinRows[kWaves][16][D + 4];
-    constexpr int kRing = NB * T::kBytes, kLds = kWaves * kRing > (int)sizeof(JoinRows) ? kWaves * kRing : sizeof(JoinRows);
+    constexpr int kRing = SHARED ? 0 : 2 * T::kBytes, kTiles = SHARED ? 2 * SharedTile<D>::kBytes : kWaves * kRing;
+    constexpr int kLds = kTiles > (int)sizeof(JoinRows) ? kTiles : sizeof(JoinRows);
     __shared__ __align__(1024) uint8_t lds[kLds];
     __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
     __shared__ int64_t sh_start[MODE == kQuota ? kQuotaBatch + 1 : 1];
@@ -670,14 +797,18 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 qf[q][s] = __builtin_bit_cast(bf16x8_t, x);
             }
         }
-        // keys that every row of the tile sees: [all_lo, all_up) and below sinks
-        const int all_up = p0 < 0 ? 0 : a.causal ? min(p0 + 1, sq.kv) : sq.kv;
-        const int all_lo = a.window > 0 ? (int)max((int64_t)p1 - a.window + 1, (int64_t)0) : 0;
+        // keys that every row of this wave sees, [all_lo, all_up) and below
+        // sinks, and that any of them does (a wave without rows: none)
+        const int pw0 = sq.kv - sq.n + min(rw, rows - 1) / a.G;
+        const int pw1 = sq.kv - sq.n + (min(rw + 16 * MT, rows) - 1) / a.G;
+        const int all_up = pw0 < 0 ? 0 : a.causal ? min(pw0 + 1, sq.kv) : sq.kv;
+        const int all_lo = a.window > 0 ? (int)max((int64_t)pw1 - a.window + 1, (int64_t)0) : 0;
 
         Sums<D, MT> sums;
 #pragma unroll
         for (int q = 0; q < MT; ++q) {
-            sums.m[q] = -INFINITY;
+            // a lane without a row (queries of 0, scores of 0) never moves
+            sums.m[q] = rw + 16 * q + m < rows ? -INFINITY : 0.f;
             sums.l[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int n = 0; n < NT; ++n) sums.o[q][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -689,97 +820,142 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
         // or behind the last are dead (their values count as 0) and the others
         // are masked row by row.
         auto whole_at = [&](int key0, const Pages& p) {
-            return p.a >= 0 && p.b >= 0 && key0 + kTile <= all_up && (key0 >= all_lo || key0 + kTile <= a.sinks);
+            return in_cache(a, p.a) && in_cache(a, p.b) && key0 + kTile <= all_up && (key0 >= all_lo || key0 + kTile <= a.sinks);
         };
         auto live_at = [&](int key0, const Pages& p) {
-            return p.of(g < 2) >= 0 ? low_bits(sq.kv - key0 - 8 * g) : 0u;
+            const bool ok0 = in_cache(a, p.a), ok1 = in_cache(a, p.b);
+            return (g < 2 ? ok0 : ok1) ? low_bits(sq.kv - key0 - 8 * g) : 0u;
         };
-        // A ring of NB tiles per wave in LDS, NB - 1 of them on their way while
-        // one is read.  The loop over common tiles (every row sees every key, no
-        // reference moves) has no other branch in it, so that the sums stay in
-        // their registers; anything else leaves it before the sums are touched.
-        // Loads past the end ask for the last tile again, so that the number
-        // under way is always the same.
-        bool wild = false;
-        int c = c0 + wk;
-        uint32_t at = 0;                           // tile c's slot
-        auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
-        auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
-        Pages pg0{}, pg1{}, pg2{}, pg3{};          // of tiles c, c + WK, ...
-        if (c < c1) {
-            pg0 = pages_for(c);
-            pg1 = pages_for(c + WK);
-            pg2 = pages_for(c + 2 * WK);
-            fetch<FMT, D, ONCE>(mine, a, pg0, tile_for(c), hk, lane);
-            fetch<FMT, D, ONCE>(mine + T::kBytes, a, pg1, tile_for(c + WK), hk, lane);
-            if constexpr (NB == 3) {
-                pg3 = pages_for(c + 3 * WK);
-                fetch<FMT, D, ONCE>(mine + 2 * T::kBytes, a, pg2, tile_for(c + 2 * WK), hk, lane);
+        if constexpr (SHARED) {
+            // The waves along the rows share every tile: one barrier each.
+            // Two waves decode the next tile's keys into operands in LDS and
+            // two its values (loaded a tile ago), while all four read this
+            // one's.
+            const int any_up = rw >= rows || pw1 < 0 ? 0 : a.causal ? min(pw1 + 1, sq.kv) : sq.kv;
+            const int any_lo = a.window > 0 ? (int)max((int64_t)pw0 - a.window + 1, (int64_t)0) : 0;
+            auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
+            auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
+            Staged<FMT, D> st;
+            int c = c0;
+            if (c < c1) {
+                st.load(a, pages_for(c), tile_for(c), hk, wave, lane);
+                st.store(lds, a, pages_for(c), tile_for(c), sq.kv, wave, lane);
+                st.load(a, pages_for(c + 1), tile_for(c + 1), hk, wave, lane);
             }
-        }
-        // the queries are used here, so that the wait for them is not left to
-        // the loops below, where it would be for the tiles' loads too
-#pragma unroll
-        for (int q = 0; q < MT; ++q)
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                u32x4_t x = __builtin_bit_cast(u32x4_t, qf[q][s]);
-                asm volatile("" : "+v"(x));
-                qf[q][s] = __builtin_bit_cast(bf16x8_t, x);
+            Pages pg0 = c < c1 ? pages_for(c) : Pages{-1, -1}, pg1 = c < c1 ? pages_for(c + 1) : pg0, pg2 = c < c1 ? pages_for(c + 2) : pg0;
+            int buf = 0;
+            auto share = [&] {
+                lds_barrier();                     // tile c is complete, and the other buffer read
+                st.store(lds + (buf ^ 1) * SharedTile<D>::kBytes, a, pg1, tile_for(c + 1), sq.kv, wave, lane);
+                st.load(a, pg2, tile_for(c + 2), hk, wave, lane);
+            };
+            auto next = [&] {
+                ++c;
+                buf ^= 1;
+                pg0 = pg1;
+                pg1 = pg2;
+                pg2 = pages_for(c + 2);
+            };
+            while (c < c1) {
+                bool shared = false;
+                while (c < c1 && whole_at(tile_at(c) * kTile, pg0)) {
+                    share();
+                    const SharedTile<D> tile{lds + buf * SharedTile<D>::kBytes + lane * 16};
+                    if (!attend_whole<D, MT>(sums, tile, qf, a.c)) {
+                        shared = true;
+                        break;
+                    }
+                    next();
+                }
+                if (c >= c1) break;
+                if (!shared) share();
+                const int key0 = tile_at(c) * kTile;
+                if (key0 < any_up && (key0 + kTile > any_lo || key0 < a.sinks)) {
+                    const SharedTile<D> tile{lds + buf * SharedTile<D>::kBytes + lane * 16};
+                    const uint32_t live = live_at(key0, pg0);
+                    if (!whole_at(key0, pg0) && __any(tile.wild(live)))
+                        attend_part<D, MT, true>(sums, tile, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                    else
+                        attend_part<D, MT, false>(sums, tile, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                }
+                next();
             }
-        // tile c is done with: its slot takes the tile NB steps on
-        auto advance = [&] {
-            fetch<FMT, D, ONCE>(mine + at, a, NB == 3 ? pg3 : pg2, tile_for(c + NB * WK), hk, lane);
-            c += WK;
-            at = at == (NB - 1) * T::kBytes ? 0 : at + T::kBytes;
-            pg0 = pg1;
-            pg1 = pg2;
-            if constexpr (NB == 3) {
-                pg2 = pg3;
-                pg3 = pages_for(c + 3 * WK);
-            } else {
+            lds_barrier();                         // the buffers are used again below
+        } else {
+            // Two tiles per wave in LDS, one on its way while the other is read (a
+            // third did not help).  The loop over common tiles (every row sees every key, no
+            // reference moves) has no other branch in it, so that the sums stay in
+            // their registers; anything else leaves it before the sums are touched.
+            // Loads past the end ask for the last tile again, so that the number
+            // under way is always the same.
+            bool wild = false;
+            int c = c0 + wk;
+            uint32_t at = 0;                           // tile c's slot
+            auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
+            auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
+            Pages pg0{}, pg1{}, pg2{};                 // of tiles c, c + WK, c + 2 WK
+            if (c < c1) {
+                pg0 = pages_for(c);
+                pg1 = pages_for(c + WK);
                 pg2 = pages_for(c + 2 * WK);
+                fetch<FMT, D, ONCE>(mine, a, pg0, tile_for(c), hk, lane);
+                fetch<FMT, D, ONCE>(mine + T::kBytes, a, pg1, tile_for(c + WK), hk, lane);
             }
-        };
-        constexpr int kUnder = (NB - 1) * T::kFetches;
-        while (c < c1) {
-            while (c < c1 && whole_at(tile_at(c) * kTile, pg0)) {
+            // the queries are used here, so that the wait for them is not left to
+            // the loops below, where it would be for the tiles' loads too
+    #pragma unroll
+            for (int q = 0; q < MT; ++q)
+    #pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    u32x4_t x = __builtin_bit_cast(u32x4_t, qf[q][s]);
+                    asm volatile("" : "+v"(x));
+                    qf[q][s] = __builtin_bit_cast(bf16x8_t, x);
+                }
+            // tile c is done with: its slot takes the next but one
+            auto advance = [&] {
+                fetch<FMT, D, ONCE>(mine + at, a, pg2, tile_for(c + 2 * WK), hk, lane);
+                c += WK;
+                at ^= T::kBytes;
+                pg0 = pg1;
+                pg1 = pg2;
+                pg2 = pages_for(c + 2 * WK);
+            };
+            constexpr int kUnder = T::kFetches;
+            while (c < c1) {
+                while (c < c1 && whole_at(tile_at(c) * kTile, pg0)) {
+                    wait_loads<kUnder>();
+                    if (!attend_whole<D, MT>(sums, RawTile<FMT, D>(base + at, lane), qf, a.c)) break;
+                    advance();
+                }
+                if (c >= c1) break;
+                // any tile
                 wait_loads<kUnder>();
-                if (!attend_whole<FMT, D, MT>(sums, base + at, lane, qf, a.c)) break;
+                const int key0 = tile_at(c) * kTile;
+                const RawTile<FMT, D> r(base + at, lane);
+                const uint32_t live = live_at(key0, pg0);
+                if (!whole_at(key0, pg0) && __any(r.wild(live))) wild = true;
+                else attend_part<D, MT, false>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
                 advance();
             }
-            if (c >= c1) break;
-            // any tile
-            wait_loads<kUnder>();
-            const int key0 = tile_at(c) * kTile;
-            Raw<FMT, D> r;
-            read_keys<FMT, D>(r, base + at, lane);
-            read_values<FMT, D>(r, base + at, lane);
-            const uint32_t live = live_at(key0, pg0);
-            if (!whole_at(key0, pg0) && __any(wild_values<FMT, D>(r, live))) wild = true;
-            else attend_part<FMT, D, MT, false>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
-            advance();
-        }
-        // tiles put off: those that rows see in part and that hold an infinite
-        // or NaN value.  Rare, and kept out of the loop above so that it costs
-        // that loop no registers.
-        if (wild) {
-            for (c = c0 + wk; c < c1; c += WK) {
-                const int key0 = tile_at(c) * kTile;
-                const Pages pc = pages_for(c);
-                if (whole_at(key0, pc)) continue;
-                wait_loads<0>();
-                fetch<FMT, D, ONCE>(mine, a, pc, tile_at(c), hk, lane);
-                wait_loads<0>();
-                Raw<FMT, D> r;
-                read_keys<FMT, D>(r, base, lane);
-                read_values<FMT, D>(r, base, lane);
-                const uint32_t live = live_at(key0, pc);
-                if (__any(wild_values<FMT, D>(r, live)))
-                    attend_part<FMT, D, MT, true>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+            // tiles put off: those that rows see in part and that hold an infinite
+            // or NaN value.  Rare, and kept out of the loop above so that it costs
+            // that loop no registers.
+            if (wild) {
+                for (c = c0 + wk; c < c1; c += WK) {
+                    const int key0 = tile_at(c) * kTile;
+                    const Pages pc = pages_for(c);
+                    if (whole_at(key0, pc)) continue;
+                    wait_loads<0>();
+                    fetch<FMT, D, ONCE>(mine, a, pc, tile_at(c), hk, lane);
+                    wait_loads<0>();
+                    const RawTile<FMT, D> r(base, lane);
+                    const uint32_t live = live_at(key0, pc);
+                    if (__any(r.wild(live)))
+                        attend_part<D, MT, true>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                }
             }
+            wait_loads<0>();                           // the ring's memory is used again below
         }
-        wait_loads<0>();                           // the ring's memory is used again below
 
         // join the waves along the keys, 16 rows of each row wave at a time
 #pragma unroll
@@ -850,7 +1026,6 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
 // 2^(m_s - m) l_s over the pieces in order.  A wave per row.
 template <int D>
 __device__ __forceinline__ void join_row(const AttnArgs& a, int per, int64_t row, int lane) {
-    constexpr int E = D / 64;                      // elements per lane
     const int t = (int)(row / a.H), h = (int)(row % a.H);
     // the sequence of row t: the last that starts at or before it
     int lo = 0, hi = a.B;
@@ -866,29 +1041,49 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int per, int64_t row
     const int64_t first = a.start[lo] * a.Hk + ((int64_t)(h / a.G) * u.sets + set) * u.tiles;
     const int w0 = (int)(first / quota), w1 = (int)((first + u.tiles - 1) / quota);
     if (w0 == w1) return;                          // written by its one workgroup
-    // pieces: of w0 from `first` on (its last unless it begins there with its
-    // units), then of each workgroup to w1 its first
-    auto piece = [&](int w) { return ((int64_t)w * 2 + (w * quota <= first)) * per + (r - set * per); };
+    // pieces: w0's last if it begins there (its first if it began before),
+    // then the first of each workgroup to w1
+    const int64_t in = r - set * per;
     const int used = w1 - w0 + 1;
+    auto at = [&](int s) { return ((int64_t)(w0 + s) * 2 + (s == 0 && w0 * quota <= first)) * per + in; };
     float top = -INFINITY;
-    for (int s = lane; s < used; s += kWave) top = fmaxf(top, a.stat[piece(w0 + s) * 2]);
+    for (int s = lane; s < used; s += kWave) top = fmaxf(top, a.stat[at(s) * 2]);
 #pragma unroll
     for (int off = kWave / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
     const float ref = top == -INFINITY ? 0.f : top;
-    float acc[E] = {}, l = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < used; ++s) {               // unrolled, so that eight loads are under way
-        const int64_t at = piece(w0 + s);
-        const float2 ml = *reinterpret_cast<const float2*>(a.stat + at * 2);
-        const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-        l += f * ml.y;
+    // D/4 lanes take 4 elements each of a piece, the wave 256/D pieces at a
+    // time and four such rounds under way
+    constexpr int L = D / 4, P = kWave / L;
+    const int sub = lane / L, d0 = lane % L * 4;
+    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+    for (int s0 = 0; s0 < used; s0 += 4 * P) {
+        f32x4_t x[4];
+        float2 ml[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += f * a.part[at * D + lane * E + e];
+        for (int i = 0; i < 4; ++i) {
+            const int s = min(s0 + i * P + sub, used - 1);
+            ml[i] = *reinterpret_cast<const float2*>(a.stat + at(s) * 2);
+            x[i] = *reinterpret_cast<const f32x4_t*>(a.part + at(s) * D + d0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (s0 + i * P + sub >= used) continue;
+            const float f = __builtin_amdgcn_exp2f(ml[i].x - ref);
+            l += f * ml[i].y;
+            acc += f * x[i];
+        }
     }
+#pragma unroll
+    for (int off = L; off < kWave; off <<= 1) {
+        l += __shfl_xor(l, off);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], off);
+    }
+    if (sub != 0) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* dst = a.out + (int64_t)t * a.os + (int64_t)h * D + lane * E;
-    if constexpr (E == 2) *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    else *dst = (uint16_t)(pack_bf16(acc[0] * inv, 0.f) & 0xFFFF);
+    *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.os + (int64_t)h * D + d0) =
+        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
 }
 
 template <int D>
@@ -901,6 +1096,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a, int per) {
 
 // Launch shape: a function of the sizes alone, so that the workspace's size
 // and the launch agree.
+// 16-row tiles of a wave where four waves along the rows share each tile of
+// keys: what 256 registers hold.
+constexpr int shared_mt(int D) { return D == 128 ? 3 : 4; }
 struct Shape {
     int mode, mt, wr, row_tiles, grid;
 };
@@ -910,9 +1108,15 @@ Shape shape_of(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c) {
     const int64_t G = p.heads / c.kv_heads;
     const int64_t mq = p.max_q < p.num_tokens ? p.max_q : p.num_tokens;
     const int64_t rows = mq * G;
-    s.mt = rows <= 16 || wide ? 1 : 2;
-    const int64_t sets = (rows + 16 * s.mt - 1) / (16 * s.mt);
-    s.wr = sets <= 1 ? 1 : sets <= 2 ? 2 : 4;
+    if (rows <= 64) {
+        // waves along the keys: 16 rows a wave, or 32; above that two waves
+        // along the rows, or four (bf16 rows of 128: 16 a wave always)
+        s.mt = rows <= 16 || wide ? 1 : 2;
+        s.wr = rows <= 16 * s.mt ? 1 : 2;
+    } else {
+        s.mt = shared_mt(c.head_dim);
+        s.wr = kWaves;
+    }
     const int64_t per = 16 * s.mt * s.wr;
     int64_t tiles = (rows + per - 1) / per;
     int64_t keys = p.max_kv;
@@ -921,11 +1125,15 @@ Shape shape_of(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c) {
         if (w < keys) keys = w;
     }
     const int64_t pairs = (int64_t)p.batch * c.kv_heads;
-    // quotas where sequences are long enough to be divided and few sets of
-    // rows share their keys
-    if (p.batch <= kQuotaBatch && rows <= 2 * per && (keys + kTile - 1) / kTile > kQuotaLeast) {
+    // Quotas where sequences are long enough to be divided and few sets of
+    // rows share their keys; not where a window makes them all alike and
+    // there are enough of them (64 sequences x 8 heads of a window of 1000:
+    // 37 us, and 38 us + 18 us for the join with quotas).
+    const int64_t held = 256 * (wide && s.wr < kWaves ? 1 : s.mt == 1 && fp4 ? 3 : 2);   // workgroups the GPU holds at once
+    const bool alike = p.window > 0 && keys < p.max_kv && pairs * tiles >= held;
+    if (p.batch <= kQuotaBatch && pairs * tiles < 2 * held && (keys + kTile - 1) / kTile > kQuotaLeast && !alike) {
         s.mode = kQuota;
-        s.grid = 256 * (wide ? 1 : s.mt == 1 && fp4 ? 3 : 2);           // what the GPU holds at once
+        s.grid = (int)held;
         return s;
     }
     s.mode = kEven;
@@ -941,12 +1149,11 @@ void launch_mode(const AttnArgs& a, const Shape& sh, hipStream_t s) {
     // waves per SIMD: what the registers of MT tiles leave
     constexpr bool fp4 = FMT == MOE_KV_MXFP4;
     constexpr int MT = !fp4 && D == 128 ? 1 : 2, W1 = !fp4 ? 2 : D == 128 ? 3 : 4, W2 = !fp4 || D == 128 ? 2 : 3;
-    constexpr int N1 = 2, N2 = fp4 ? 3 : 2;
     const dim3 grid(sh.grid), block(kThreads);
-    if (sh.mt == 1 && sh.wr == 1) hipLaunchKernelGGL((k_attn<FMT, D, 1, 1, N1, W1, MODE>), grid, block, 0, s, a);
-    else if (sh.wr == 1) hipLaunchKernelGGL((k_attn<FMT, D, MT, 1, N2, W2, MODE>), grid, block, 0, s, a);
-    else if (sh.wr == 2) hipLaunchKernelGGL((k_attn<FMT, D, MT, 2, N2, W2, MODE>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_attn<FMT, D, MT, 4, N2, W2, MODE>), grid, block, 0, s, a);
+    if (sh.mt == 1 && sh.wr == 1) hipLaunchKernelGGL((k_attn<FMT, D, 1, 1, W1, MODE>), grid, block, 0, s, a);
+    else if (sh.wr == 1) hipLaunchKernelGGL((k_attn<FMT, D, MT, 1, W2, MODE>), grid, block, 0, s, a);
+    else if (sh.wr == 2) hipLaunchKernelGGL((k_attn<FMT, D, MT, 2, W2, MODE>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_attn<FMT, D, shared_mt(D), kWaves, 2, MODE>), grid, block, 0, s, a);
 }
 
 template <int FMT, int D>
