@@ -153,34 +153,43 @@ __device__ __forceinline__ Pages pages_of(const AttnArgs& a, ScalarInts row, int
 }
 __device__ __forceinline__ bool in_cache(const AttnArgs& a, int page) { return (unsigned)page < (unsigned)a.num_pages; }
 
+typedef __attribute__((address_space(3))) void lds_void;
+
 // 16 (or 4) bytes per lane from base + off (base the same for all lanes)
 // straight into LDS: lane L's go to lds + 16 L (4 L).  These loads write no
 // register, so nothing the compiler allocates can be under way; it does not
 // count them either, which is the point: of a ring slot chosen at run time it
 // would assume that any load under way may write it, and wait for all of them
 // before a read.  wait_loads() below does the waiting, before every read.
+// m0 holds the LDS address; the compiler writes m0 only right before its own
+// uses, of which there are none in this file, so it is not preserved.
 // ONCE: no other wave reads these bytes, so they need not stay in the caches
 // (nt): 5.6 against 4.7 TB/s of such loads alone over 0.7 GB of MXFP4 keys.
 template <bool ONCE>
 __device__ __forceinline__ void lds_dma16(const uint8_t* base, uint32_t off, uint32_t lds) {
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    const uint64_t s = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
+    const uint32_t m = __builtin_amdgcn_readfirstlane((int)lds);
     if constexpr (ONCE)
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(off), "s"(base)
-                     : "memory", "m0");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(m), "v"(off), "s"(s) : "memory");
     else
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                     : "memory", "m0");
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(m), "v"(off), "s"(s) : "memory");
 }
 __device__ __forceinline__ void lds_dma16(const uint8_t* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+    const uint32_t m = __builtin_amdgcn_readfirstlane((int)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(m), "v"(src) : "memory");
 }
 __device__ __forceinline__ void lds_dma4(const uint8_t* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "memory", "m0");
+    const uint32_t m = __builtin_amdgcn_readfirstlane((int)lds);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m), "v"(src) : "memory");
 }
 
 // Starts the loads of a tile into its slot dst (an LDS address, the same for
-// all lanes).  What this wave read from the slot before has arrived.
-template <int FMT, int D, bool ONCE>
-__device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pages& pg, int tile, int hk, int lane) {
+// all lanes); of WAVES waves that share the tile, the `part`-th of them starts
+// its share.  What this wave read from the slot before has arrived.
+template <int FMT, int D, int WAVES, bool ONCE>
+__device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pages& pg, int tile, int hk, int lane, int part) {
     using T = Tile<FMT, D>;
     const int mask = (1 << a.shift) - 1;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -191,33 +200,40 @@ __device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pag
         // chunk c of row r is stored at c ^ (r / 8)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            lds_dma16<ONCE>(a.k + (h ? b1 : b0) * 64, lane / 4 * 64 + ((lane % 4) ^ (2 * h + lane / 32)) * 16, dst + h * 1024);
+            if (WAVES == 1 || part == h)
+                lds_dma16<ONCE>(a.k + (h ? b1 : b0) * 64, lane / 4 * 64 + ((lane % 4) ^ (2 * h + lane / 32)) * 16, dst + h * 1024);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) lds_dma16<ONCE>(a.v + (h ? b1 : b0) * 64, lane * 16, dst + T::kValues + h * 1024);
-        const uint8_t* sc = lane < 32 ? a.ks : a.vs;
-        lds_dma4(sc + (lane & 16 ? b1 : b0) * 4 + lane % 16 * 4, dst + T::kScales);
+        for (int h = 0; h < 2; ++h)
+            if (WAVES == 1 || part == 2 + h) lds_dma16<ONCE>(a.v + (h ? b1 : b0) * 64, lane * 16, dst + T::kValues + h * 1024);
+        if (WAVES == 1 || part == 3) {
+            const uint8_t* sc = lane < 32 ? a.ks : a.vs;
+            lds_dma4(sc + (lane & 16 ? b1 : b0) * 4 + lane % 16 * 4, dst + T::kScales);
+        }
     } else if constexpr (FMT == MOE_KV_MXFP4) {
         const int64_t base = lane < 32 ? b0 : b1;
         const int chunk = (lane % 2) ^ ((lane / 16) & 1);               // chunk c of row r at c ^ (r / 8 mod 2)
-        lds_dma16(a.k + base * 32 + (lane / 2 % 16 * 32 + chunk * 16), dst);
-        lds_dma16(a.v + base * 32 + lane % 32 * 16, dst + T::kValues);
-        const uint8_t* sc = lane & 16 ? a.vs : a.ks;                    // lanes 32.. repeat lanes 0..31
-        lds_dma4(sc + (lane & 8 ? b1 : b0) * 2 + lane % 8 * 4, dst + T::kScales);
+        if (WAVES == 1 || part == 0) lds_dma16(a.k + base * 32 + (lane / 2 % 16 * 32 + chunk * 16), dst);
+        if (WAVES == 1 || part == 1) lds_dma16(a.v + base * 32 + lane % 32 * 16, dst + T::kValues);
+        if (WAVES == 1 || part == 2) {
+            const uint8_t* sc = lane & 16 ? a.vs : a.ks;                // lanes 32.. repeat lanes 0..31
+            lds_dma4(sc + (lane & 8 ? b1 : b0) * 2 + lane % 8 * 4, dst + T::kScales);
+        }
     } else {
-        constexpr int C = D / 8, R = 64 / C;                            // chunks per row, rows per load
+        constexpr int C = D / 8, R = 64 / C, N = kTile / R;             // chunks per row, rows per load, loads
 #pragma unroll
-        for (int i = 0; i < kTile / R; ++i) {
+        for (int i = 0; i < N; ++i) {
+            if (WAVES > 1 && part != i * WAVES / N) continue;
             // chunk c of row r at c ^ (its lane m = 4 (r / 8) + r mod 4)
             const int row = i * R + lane / C, mm = 4 * (row / 8) + row % 4;
             lds_dma16<ONCE>(a.k + (i < 16 / R ? b0 : b1) * (2 * D), row % 16 * (2 * D) + ((lane % C) ^ (mm % C)) * 16, dst + i * 1024);
         }
 #pragma unroll
-        for (int i = 0; i < kTile / R; ++i)
+        for (int i = 0; i < N; ++i) {
+            if (WAVES > 1 && part != i * WAVES / N) continue;
             lds_dma16<ONCE>(a.v + (i < 16 / R ? b0 : b1) * (2 * D) + i % (16 / R) * 1024, lane * 16, dst + T::kValues + i * 1024);
+        }
     }
 }
-
-typedef __attribute__((address_space(3))) void lds_void;
 
 // Waits until at most N loads of this wave are under way (they end in order).
 template <int N>
@@ -463,6 +479,8 @@ template <int D> struct SharedTile {
     __device__ __forceinline__ void anew() {}
 };
 
+__device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
+
 // The common tile: every row sees every key.  False, with the sums untouched,
 // if a reference has to move.
 template <int D, int MT, typename Src>
@@ -481,6 +499,38 @@ __device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const Src& src, 
 #pragma unroll
         for (int q = 0; q < MT; ++q) sums.o[q][n] = mfma(v, pf[q], sums.o[q][n]);
     });
+    return true;
+}
+
+// The same of a shared tile, all of a product's operands asked for before its
+// first: read one by one, each would wait for LDS longer than its MT matrix
+// instructions last.  The values' reads pass under the softmax.
+template <int D, int MT>
+__device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const SharedTile<D>& src, const bf16x8_t (&qf)[MT][D / 32],
+                                             float c) {
+    constexpr int KS = D / 32, NT = D / 16;
+    bf16x8_t kf[2 * KS], vf[NT];
+#pragma unroll
+    for (int i = 0; i < 2 * KS; ++i) kf[i] = src.at(i);
+    pin();
+    f32x4_t sc[MT][2];
+    scores<D, MT>(sc, [&](int t, int s) { return kf[t * KS + s]; }, qf);
+    pin();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) vf[n] = src.at(2 * KS + n);
+    pin();
+    float top[MT];
+    tops<MT>(top, sc, c);
+    bool move = false;
+#pragma unroll
+    for (int q = 0; q < MT; ++q) move |= top[q] > sums.m[q] + kSlack;
+    if (__any(move)) return false;
+    bf16x8_t pf[MT];
+    weights<D, MT>(sums, pf, sc, c);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < MT; ++q) sums.o[q][n] = mfma(vf[n], pf[q], sums.o[q][n]);
     return true;
 }
 
@@ -540,88 +590,54 @@ __device__ __forceinline__ void attend_part(Sums<D, MT>& a, const Src& src, cons
     }
 }
 
-// A share of a tile on its way from memory to operands in LDS: waves 0 and 1
-// take the keys of a half tile each, 2 and 3 half of the values' elements.
-template <int FMT, int D> struct Staged {
-    static constexpr bool kFp4 = FMT == MOE_KV_MXFP4;
-    static constexpr int KW = kFp4 ? D / 32 : D / 8;                    // words of a lane's key
-    static constexpr int VW = kFp4 ? D / 16 : 8 * (D / 64);             // and of its values
-    uint32_t w[KW > VW ? KW : VW];
-    uint32_t sb[2];                                // scale bytes
-    __device__ __forceinline__ void load(const AttnArgs& a, const Pages& pg, int tile, int hk, int wave, int lane) {
-        const int m = lane % 16, g = lane / 16, mask = (1 << a.shift) - 1;
-        const int pa = in_cache(a, pg.a) ? pg.a : 0, pb = in_cache(a, pg.b) ? pg.b : 0;
-        if (wave < 2) {
-            const int64_t base = ((int64_t)(m < 8 ? pa : pb) * a.Hk + hk) << a.shift;
-            const int64_t row = base + ((tile * kTile + 8 * (m / 4) + 4 * wave + m % 4) & mask);
-            if constexpr (kFp4) {
-                load_words<KW>(w, a.k + row * (D / 2) + g * (D / 8));
-                sb[0] = a.ks[row * (D / 32) + g * D / 128];
-            } else {
-                load_words<KW>(w, a.k + (row * D + g * (D / 4)) * 2);
-            }
-        } else {
-            const int64_t base = ((int64_t)(g < 2 ? pa : pb) * a.Hk + hk) << a.shift;
-            const int row = (tile * kTile + 8 * g) & mask;
-            if constexpr (kFp4) {
-                constexpr int KG = v_keys_per_piece(D);
+// A wave's share of turning a tile as fetched (raw) into operands (dst): waves 0
+// and 1 take the keys of a half tile each, 2 and 3 half of the elements of the
+// values.  live: which of the lane group's 8 keys exist.
+template <int FMT, int D, int HALF>
+__device__ __forceinline__ void share_keys(const uint8_t* raw, uint8_t* dst, int lane) {
+    const int m = lane % 16, g = lane / 16, row = 8 * (m / 4) + 4 * HALF + m % 4;
+    const uint8_t* p = raw + row * Tile<FMT, D>::kRowBytes;
+    uint8_t* to = dst + HALF * (D / 32) * 1024 + lane * 16;
+    if constexpr (FMT == MOE_KV_MXFP4) {
+        uint32_t w[D / 32];
+        if constexpr (D == 128) load_words<4>(w, p + (g ^ (m / 4)) * 16);
+        else load_words<2>(w, p + ((g / 2) ^ ((m / 4) & 1)) * 16 + g % 2 * 8);
+        const float sc = e8m0_as_scale(raw[Tile<FMT, D>::kScales + row * (D / 32) + g * D / 128]);
 #pragma unroll
-                for (int i = 0; i < 8 / KG; ++i)
-                    load_words<4>(w + 4 * i, a.v + base * (D / 2) + (row / KG + i) * (KG * D / 2) + m * 16);
-                const uint2 b = *reinterpret_cast<const uint2*>(a.vs + base * (D / 32) + row * (D / 32) + (m * D / 512) * 8);
-                sb[0] = b.x; sb[1] = b.y;
-            } else {
+        for (int s = 0; s < D / 32; ++s) *reinterpret_cast<bf16x8_t*>(to + s * 1024) = decode8_bf16(w[s], sc);
+    } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    load_words<D / 64>(w + j * (D / 64), a.v + ((base + row + j) * D + m * (D / 16) + (wave - 2) * (D / 32)) * 2);
-            }
-        }
+        for (int s = 0; s < D / 32; ++s)
+            *reinterpret_cast<u32x4_t*>(to + s * 1024) = *reinterpret_cast<const u32x4_t*>(p + ((g * (D / 32) + s) ^ (m % (D / 8))) * 16);
     }
-    __device__ __forceinline__ void store(uint8_t* dst, const AttnArgs& a, const Pages& pg, int tile, int kv, int wave, int lane) {
-        const int g = lane / 16;
-        if (wave < 2) {
-            uint8_t* to = dst + wave * (D / 32) * 1024 + lane * 16;
-#pragma unroll
-            for (int s = 0; s < D / 32; ++s) {
-                if constexpr (kFp4)
-                    *reinterpret_cast<bf16x8_t*>(to + s * 1024) = decode8_bf16(w[s], e8m0_as_scale(sb[0]));
-                else
-                    *reinterpret_cast<u32x4_t*>(to + s * 1024) = u32x4_t{w[4 * s], w[4 * s + 1], w[4 * s + 2], w[4 * s + 3]};
-            }
-            return;
-        }
-        const int key0 = tile * kTile;
-        const bool ok0 = in_cache(a, pg.a), ok1 = in_cache(a, pg.b);
-        const uint32_t live = (g < 2 ? ok0 : ok1) ? low_bits(kv - key0 - 8 * g) : 0u;
-        uint8_t* to = dst + 2 * (D / 32) * 1024 + lane * 16;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            const int u = (wave - 2) * (D / 64) + i;                    // this wave's pairs of elements
-            uint32_t x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (kFp4) {
-                    const uint32_t b = sb[j / 4];
-                    const float sc = __uint_as_float(j % 4 == 3 ? b >> 1 : b << (23 - 8 * (j % 4)));
-                    // the pair's byte of key j, brought down: which one depends on the wave
-                    const int at = j * (D / 32);
-                    x[j] = decode2<0>(w[at / 4] >> (8 * (at % 4) + 8 * u), sc);
-                } else {
-                    x[j] = w[j * (D / 64) + i];
-                }
-                x[j] = (live >> j) & 1 ? x[j] : 0;
-            }
-            u32x4_t lo, hi;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                lo[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x05040100u);
-                hi[k] = __builtin_amdgcn_perm(x[2 * k + 1], x[2 * k], 0x07060302u);
-            }
-            *reinterpret_cast<u32x4_t*>(to + (2 * u) * 1024) = lo;
-            *reinterpret_cast<u32x4_t*>(to + (2 * u + 1) * 1024) = hi;
-        }
+}
+template <int FMT, int D, int HALF>
+__device__ __forceinline__ void share_values(const uint8_t* raw, uint8_t* dst, uint32_t live, int lane) {
+    Raw<FMT, D> r;
+    read_values<FMT, D>(r, raw, lane);
+    uint8_t* to = dst + 2 * (D / 32) * 1024 + lane * 16;
+    auto pair = [&](auto U) {
+        constexpr int u = decltype(U)::value;
+        bf16x8_t x, y;
+        v_operand<FMT, D, u>(r, live, x, y);
+        *reinterpret_cast<bf16x8_t*>(to + 2 * u * 1024) = x;
+        *reinterpret_cast<bf16x8_t*>(to + (2 * u + 1) * 1024) = y;
+    };
+    pair(std::integral_constant<int, HALF * (D / 64)>{});
+    if constexpr (D == 128) pair(std::integral_constant<int, HALF * (D / 64) + 1>{});
+}
+template <int FMT, int D>
+__device__ __forceinline__ void share_out(const uint8_t* raw, uint8_t* dst, uint32_t live, bool all_live, int wave, int lane) {
+    if (wave == 0) {
+        share_keys<FMT, D, 0>(raw, dst, lane);
+    } else if (wave == 1) {
+        share_keys<FMT, D, 1>(raw, dst, lane);
+    } else {
+        if (all_live) live = 0xFF;
+        if (wave == 2) share_values<FMT, D, 0>(raw, dst, live, lane);
+        else share_values<FMT, D, 1>(raw, dst, live, lane);
     }
-};
+}
 
 // A workgroup barrier that waits for this wave's LDS operations only: loads
 // from memory stay under way.
@@ -668,7 +684,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
     constexpr bool SHARED = WR == kWaves;          // or by all four, at the same time
     using T = Tile<FMT, D>;
     typedef float JoinRows[kWaves][16][D + 4];
-    constexpr int kRing = SHARED ? 0 : 2 * T::kBytes, kTiles = SHARED ? 2 * SharedTile<D>::kBytes : kWaves * kRing;
+    constexpr int kRing = SHARED ? 0 : 2 * T::kBytes, kTiles = SHARED ? 2 * (SharedTile<D>::kBytes + T::kBytes) : kWaves * kRing;
     constexpr int kLds = kTiles > (int)sizeof(JoinRows) ? kTiles : sizeof(JoinRows);
     __shared__ __align__(1024) uint8_t lds[kLds];
     __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
@@ -679,7 +695,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
     const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wr = wave % WR, wk = wave / WR;
     const uint8_t* const base = lds + wave * kRing;
-    const uint32_t mine = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)(lds + wave * kRing));
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void*)lds, mine = lds_at + wave * kRing;
     const int m = lane % 16, g = lane / 16;
     const ScalarInts cu_q = (ScalarInts)(uintptr_t)a.cu_q, kv_lens = (ScalarInts)(uintptr_t)a.kv_lens;
 
@@ -827,27 +843,37 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             return (g < 2 ? ok0 : ok1) ? low_bits(sq.kv - key0 - 8 * g) : 0u;
         };
         if constexpr (SHARED) {
-            // The waves along the rows share every tile: one barrier each.
-            // Two waves decode the next tile's keys into operands in LDS and
-            // two its values (loaded a tile ago), while all four read this
-            // one's.
+            // The waves along the rows share every tile.  Between two barriers
+            // they start the loads of the tile after the next, turn the next one,
+            // which has arrived, into operands, and read this one's.
             const int any_up = rw >= rows || pw1 < 0 ? 0 : a.causal ? min(pw1 + 1, sq.kv) : sq.kv;
             const int any_lo = a.window > 0 ? (int)max((int64_t)pw0 - a.window + 1, (int64_t)0) : 0;
             auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
             auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
-            Staged<FMT, D> st;
-            int c = c0;
+            uint8_t* const raws = lds + 2 * SharedTile<D>::kBytes;
+            const uint32_t raw_at = lds_at + 2 * SharedTile<D>::kBytes;
+            auto turn = [&](int slot, const Pages& p, int tile) {
+                const int key0 = tile * kTile;
+                const bool all = in_cache(a, p.a) && in_cache(a, p.b) && key0 + kTile <= sq.kv;
+                share_out<FMT, D>(raws + slot * T::kBytes, lds + slot * SharedTile<D>::kBytes, all ? 0u : live_at(key0, p), all, wave, lane);
+            };
+            int c = c0, buf = 0;                   // tile and its slot
+            Pages pg0{}, pg1{}, pg2{};             // of tiles c, c + 1, c + 2
             if (c < c1) {
-                st.load(a, pages_for(c), tile_for(c), hk, wave, lane);
-                st.store(lds, a, pages_for(c), tile_for(c), sq.kv, wave, lane);
-                st.load(a, pages_for(c + 1), tile_for(c + 1), hk, wave, lane);
+                pg0 = pages_for(c);
+                pg1 = pages_for(c + 1);
+                pg2 = pages_for(c + 2);
+                fetch<FMT, D, kWaves, false>(raw_at, a, pg0, tile_for(c), hk, lane, wave);
+                fetch<FMT, D, kWaves, false>(raw_at + T::kBytes, a, pg1, tile_for(c + 1), hk, lane, wave);
+                wait_loads<0>();
+                lds_barrier();
+                turn(0, pg0, tile_for(c));
             }
-            Pages pg0 = c < c1 ? pages_for(c) : Pages{-1, -1}, pg1 = c < c1 ? pages_for(c + 1) : pg0, pg2 = c < c1 ? pages_for(c + 2) : pg0;
-            int buf = 0;
             auto share = [&] {
-                lds_barrier();                     // tile c is complete, and the other buffer read
-                st.store(lds + (buf ^ 1) * SharedTile<D>::kBytes, a, pg1, tile_for(c + 1), sq.kv, wave, lane);
-                st.load(a, pg2, tile_for(c + 2), hk, wave, lane);
+                wait_loads<0>();                   // tile c + 1 has arrived, this wave's part of it
+                lds_barrier();                     // and the others'; tile c is operands, c - 1 read
+                fetch<FMT, D, kWaves, false>(raw_at + buf * T::kBytes, a, pg2, tile_for(c + 2), hk, lane, wave);
+                turn(buf ^ 1, pg1, tile_for(c + 1));
             };
             auto next = [&] {
                 ++c;
@@ -880,6 +906,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 }
                 next();
             }
+            wait_loads<0>();
             lds_barrier();                         // the buffers are used again below
         } else {
             // Two tiles per wave in LDS, one on its way while the other is read (a
@@ -898,8 +925,8 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 pg0 = pages_for(c);
                 pg1 = pages_for(c + WK);
                 pg2 = pages_for(c + 2 * WK);
-                fetch<FMT, D, ONCE>(mine, a, pg0, tile_for(c), hk, lane);
-                fetch<FMT, D, ONCE>(mine + T::kBytes, a, pg1, tile_for(c + WK), hk, lane);
+                fetch<FMT, D, 1, ONCE>(mine, a, pg0, tile_for(c), hk, lane, 0);
+                fetch<FMT, D, 1, ONCE>(mine + T::kBytes, a, pg1, tile_for(c + WK), hk, lane, 0);
             }
             // the queries are used here, so that the wait for them is not left to
             // the loops below, where it would be for the tiles' loads too
@@ -913,7 +940,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 }
             // tile c is done with: its slot takes the next but one
             auto advance = [&] {
-                fetch<FMT, D, ONCE>(mine + at, a, pg2, tile_for(c + 2 * WK), hk, lane);
+                fetch<FMT, D, 1, ONCE>(mine + at, a, pg2, tile_for(c + 2 * WK), hk, lane, 0);
                 c += WK;
                 at ^= T::kBytes;
                 pg0 = pg1;
@@ -946,7 +973,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                     const Pages pc = pages_for(c);
                     if (whole_at(key0, pc)) continue;
                     wait_loads<0>();
-                    fetch<FMT, D, ONCE>(mine, a, pc, tile_at(c), hk, lane);
+                    fetch<FMT, D, 1, ONCE>(mine, a, pc, tile_at(c), hk, lane, 0);
                     wait_loads<0>();
                     const RawTile<FMT, D> r(base, lane);
                     const uint32_t live = live_at(key0, pc);
