@@ -47,7 +47,7 @@ struct AttnArgs {
     const int32_t *table, *cu_q, *kv_lens;
     const uint8_t *k, *v, *ks, *vs;
     float *part, *stat;                            // pieces: sums [workgroup][2][rows][D], (reference, sum of weights)
-    int64_t* start;                                // [B + 2]: first unit of each sequence per head, and the quota
+    int32_t* joins;                                // [workgroup][kJoinInts]: the rows that its last piece begins
     int64_t qs, os;
     int32_t B, T, H, Hk, G, W, shift, num_pages, causal, window, sinks;
     int32_t row_tiles;                             // even: workgroups along the rows of a sequence and head
@@ -632,9 +632,11 @@ __device__ __forceinline__ void share_out(const uint8_t* raw, uint8_t* dst, uint
         share_keys<FMT, D, 0>(raw, dst, lane);
     } else if (wave == 1) {
         share_keys<FMT, D, 1>(raw, dst, lane);
+    } else if (wave == 2) {
+        if (all_live) share_values<FMT, D, 0>(raw, dst, 0xFF, lane);
+        else share_values<FMT, D, 0>(raw, dst, live, lane);
     } else {
-        if (all_live) live = 0xFF;
-        if (wave == 2) share_values<FMT, D, 0>(raw, dst, live, lane);
+        if (all_live) share_values<FMT, D, 1>(raw, dst, 0xFF, lane);
         else share_values<FMT, D, 1>(raw, dst, live, lane);
     }
 }
@@ -653,6 +655,7 @@ __device__ __forceinline__ void lds_barrier() {
 // the sequences, since only the device knows the lengths.
 enum { kEven, kQuota };
 constexpr int kQuotaBatch = 1024;                  // sequences kQuota handles: four per thread, their sums in LDS
+constexpr int kJoinInts = 8;
 constexpr int kQuotaLeast = 16;                    // units a workgroup takes at least, where a sequence has them
 
 // A sequence's sets of `per` rows, and the units each counts: as many tiles of
@@ -700,7 +703,9 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
     const ScalarInts cu_q = (ScalarInts)(uintptr_t)a.cu_q, kv_lens = (ScalarInts)(uintptr_t)a.kv_lens;
 
     // this workgroup's units [unit, last)
-    int64_t unit, last;
+    int64_t unit, last, quota = 1;
+    int joined = 0;                                // pieces of the rows that the last piece here begins
+    int join_start = 0, join_r0 = 0, join_rows = 0, join_hk = 0;
     if constexpr (MODE == kQuota) {
         int64_t before[4], sum = 0;
         int most = 0;
@@ -739,14 +744,10 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             if (tid * 4 + i <= a.B) sh_start[tid * 4 + i] = ahead + incl - sum + before[i];
         if (tid == 0) sh_start[a.B] = all;
         const int64_t share = (all * a.Hk + gridDim.x - 1) / gridDim.x;
-        const int64_t quota = max(share, (int64_t)min(most, kQuotaLeast));
+        quota = max(share, (int64_t)min(most, kQuotaLeast));
         unit = blockIdx.x * quota;
         last = min(unit + quota, all * a.Hk);
         __syncthreads();
-        if (blockIdx.x == 0) {                     // for the join
-            for (int b = tid; b <= a.B; b += kThreads) a.start[b] = sh_start[b];
-            if (tid == 0) a.start[a.B + 1] = quota;
-        }
     } else {
         unit = blockIdx.x;                         // set of rows, then by row_tiles
         last = INT64_MAX;
@@ -776,6 +777,13 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             c0 = __builtin_amdgcn_readfirstlane((int)(rest - (int64_t)set * u.tiles));
             c1 = (int)min((int64_t)u.tiles, c0 + (last - unit));
             complete = c0 == 0 && c1 == u.tiles;
+            if (c0 == 0 && !complete) {
+                joined = (int)((unit + u.tiles - 1) / quota) - (int)blockIdx.x + 1;
+                join_start = sq.start;
+                join_r0 = set * ROWS;
+                join_rows = rows;
+                join_hk = hk;
+            }
             unit += c1 - c0;
         } else {
             const int in = (int)(blockIdx.x % (unsigned)(a.row_tiles * a.Hk));
@@ -1047,78 +1055,75 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
         }
         __syncthreads();                           // the next rows' tiles come where the join was read
     }
+    if (MODE == kQuota && tid == 0) {
+        int32_t* j = a.joins + (int64_t)blockIdx.x * kJoinInts;
+        j[0] = joined;
+        j[1] = join_start;
+        j[2] = join_r0;
+        j[3] = join_rows;
+        j[4] = join_hk;
+    }
 }
 
 // Rows whose units several workgroups shared: out = sum 2^(m_s - m) O_s / sum
-// 2^(m_s - m) l_s over the pieces in order.  A wave per row.
+// 2^(m_s - m) l_s over the pieces in order.  They begin as the last piece of
+// workgroup w and go on as the first of each that follows, so blockIdx.y = w
+// finds them in one record; blockIdx.x takes 4 `each` of its rows, a wave one
+// after the other.  This way round, a long sequence's rows are spread over the
+// XCDs: begun every 64th workgroup, they would else all be read by one.
 template <int D>
-__device__ __forceinline__ void join_row(const AttnArgs& a, int per, int64_t row, int lane) {
-    const int t = (int)(row / a.H), h = (int)(row % a.H);
-    // the sequence of row t: the last that starts at or before it
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
-    }
-    const Seq sq = sequence(a, lo, a.cu_q, a.kv_lens);
-    if (t < sq.start || t >= sq.start + sq.n) return;
-    const int r = (t - sq.start) * a.G + h % a.G, set = r / per;
-    const Units u = units_of(a, sq, per);
-    const int64_t quota = a.start[a.B + 1];
-    const int64_t first = a.start[lo] * a.Hk + ((int64_t)(h / a.G) * u.sets + set) * u.tiles;
-    const int w0 = (int)(first / quota), w1 = (int)((first + u.tiles - 1) / quota);
-    if (w0 == w1) return;                          // written by its one workgroup
-    // pieces: w0's last if it begins there (its first if it began before),
-    // then the first of each workgroup to w1
-    const int64_t in = r - set * per;
-    const int used = w1 - w0 + 1;
-    auto at = [&](int s) { return ((int64_t)(w0 + s) * 2 + (s == 0 && w0 * quota <= first)) * per + in; };
-    float top = -INFINITY;
-    for (int s = lane; s < used; s += kWave) top = fmaxf(top, a.stat[at(s) * 2]);
+__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a, int per, int each) {
+    const int w = blockIdx.y, lane = threadIdx.x % kWave;
+    const int32_t* j = a.joins + (int64_t)w * kJoinInts;
+    const int used = j[0];
+    if (used == 0) return;
+    const int start = j[1], r0 = j[2], rows = j[3], hk = j[4];
+    const int first = (blockIdx.x * kWaves + threadIdx.x / kWave) * each;
+    for (int in = first; in < min(first + each, per); ++in) {
+        const int r = r0 + in;
+        if (r >= rows) return;
+        auto at = [&](int s) { return ((int64_t)(w + s) * 2 + (s == 0)) * per + in; };
+        float top = -INFINITY;
+        for (int s = lane; s < used; s += kWave) top = fmaxf(top, a.stat[at(s) * 2]);
 #pragma unroll
-    for (int off = kWave / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    const float ref = top == -INFINITY ? 0.f : top;
-    // D/4 lanes take 4 elements each of a piece, the wave 256/D pieces at a
-    // time and four such rounds under way
-    constexpr int L = D / 4, P = kWave / L;
-    const int sub = lane / L, d0 = lane % L * 4;
-    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    for (int s0 = 0; s0 < used; s0 += 4 * P) {
-        f32x4_t x[4];
-        float2 ml[4];
+        for (int off = kWave / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+        const float ref = top == -INFINITY ? 0.f : top;
+        // D/4 lanes take 4 elements each of a piece, the wave 256/D pieces at a
+        // time and 4 or 8 such rounds under way (16 take registers that cost
+        // the short joins more than the long ones gain)
+        constexpr int L = D / 4, P = kWave / L;
+        const int sub = lane / L, d0 = lane % L * 4;
+        f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+        float l = 0.f;
+        auto add = [&](auto N, int s0) {
+            f32x4_t x[N];
+            float2 ml[N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int s = min(s0 + i * P + sub, used - 1);
-            ml[i] = *reinterpret_cast<const float2*>(a.stat + at(s) * 2);
-            x[i] = *reinterpret_cast<const f32x4_t*>(a.part + at(s) * D + d0);
+            for (int i = 0; i < N; ++i) {
+                const int s = min(s0 + i * P + sub, used - 1);
+                ml[i] = *reinterpret_cast<const float2*>(a.stat + at(s) * 2);
+                x[i] = *reinterpret_cast<const f32x4_t*>(a.part + at(s) * D + d0);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float f = s0 + i * P + sub < used ? __builtin_amdgcn_exp2f(ml[i].x - ref) : 0.f;
+                l += f * ml[i].y;
+                acc += f * x[i];
+            }
+        };
+        if (used <= 4 * P) add(std::integral_constant<int, 4>{}, 0);
+        else for (int s0 = 0; s0 < used; s0 += 8 * P) add(std::integral_constant<int, 8>{}, s0);
+#pragma unroll
+        for (int off = L; off < kWave; off <<= 1) {
+            l += __shfl_xor(l, off);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], off);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (s0 + i * P + sub >= used) continue;
-            const float f = __builtin_amdgcn_exp2f(ml[i].x - ref);
-            l += f * ml[i].y;
-            acc += f * x[i];
-        }
+        if (sub != 0) continue;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(a.out + (int64_t)(start + r / a.G) * a.os + (int64_t)(hk * a.G + r % a.G) * D + d0) =
+            make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
     }
-#pragma unroll
-    for (int off = L; off < kWave; off <<= 1) {
-        l += __shfl_xor(l, off);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], off);
-    }
-    if (sub != 0) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(a.out + (int64_t)t * a.os + (int64_t)h * D + d0) =
-        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-}
-
-template <int D>
-__global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a, int per) {
-    const int lane = threadIdx.x % kWave;
-    for (int64_t row = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave; row < (int64_t)a.T * a.H;
-         row += (int64_t)gridDim.x * kWaves)
-        join_row<D>(a, per, row, lane);
 }
 
 // Launch shape: a function of the sizes alone, so that the workspace's size
@@ -1158,7 +1163,7 @@ Shape shape_of(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c) {
     // 37 us, and 38 us + 18 us for the join with quotas).
     const int64_t held = 256 * (wide && s.wr < kWaves ? 1 : s.mt == 1 && fp4 ? 3 : 2);   // workgroups the GPU holds at once
     const bool alike = p.window > 0 && keys < p.max_kv && pairs * tiles >= held;
-    if (p.batch <= kQuotaBatch && pairs * tiles < 2 * held && (keys + kTile - 1) / kTile > kQuotaLeast && !alike) {
+    if (p.batch <= kQuotaBatch && pairs * tiles < held && (keys + kTile - 1) / kTile > kQuotaLeast && !alike) {
         s.mode = kQuota;
         s.grid = (int)held;
         return s;
@@ -1192,9 +1197,9 @@ hipError_t launch_fmt(const AttnArgs& a, const Shape& sh, hipStream_t s) {
     launch_mode<FMT, D, kQuota>(a, sh, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t wgs = ((int64_t)a.T * a.H + kWaves - 1) / kWaves;
-    hipLaunchKernelGGL((k_attn_join<D>), dim3((unsigned)(wgs < 65536 ? wgs : 65536)), dim3(kThreads), 0, s, a,
-                       16 * sh.mt * sh.wr);
+    const int per = 16 * sh.mt * sh.wr, each = per > 64 ? 4 : 1;        // many rows have few pieces
+    hipLaunchKernelGGL((k_attn_join<D>), dim3((per + kWaves * each - 1) / (kWaves * each), sh.grid), dim3(kThreads), 0, s, a,
+                       per, each);
     return hipGetLastError();
 }
 
@@ -1206,7 +1211,7 @@ int64_t piece_rows(const Shape& s) { return (int64_t)s.grid * 2 * 16 * s.mt * s.
 size_t attention_workspace_bytes(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c) {
     const Shape s = shape_of(p, c);
     if (s.mode == kEven) return 0;
-    return piece_rows(s) * (c.head_dim + 2) * sizeof(float) + ((size_t)p.batch + 2) * sizeof(int64_t);
+    return piece_rows(s) * (c.head_dim + 2) * sizeof(float) + (size_t)s.grid * kJoinInts * sizeof(int32_t);
 }
 
 hipError_t launch_attention(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c, void* workspace,
@@ -1220,7 +1225,7 @@ hipError_t launch_attention(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cac
     if (sh.mode == kQuota) {
         a.part = static_cast<float*>(workspace);
         a.stat = a.part + piece_rows(sh) * c.head_dim;
-        a.start = reinterpret_cast<int64_t*>(a.stat + piece_rows(sh) * 2);
+        a.joins = reinterpret_cast<int32_t*>(a.stat + piece_rows(sh) * 2);
     }
     a.qs = p.q_stride; a.os = p.out_stride;
     a.B = p.batch; a.T = p.num_tokens; a.H = p.heads; a.Hk = c.kv_heads; a.G = p.heads / c.kv_heads;
