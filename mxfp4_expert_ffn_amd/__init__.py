@@ -500,16 +500,33 @@ def _like(t, dtype, shape, device, name):
 def _heads(t, D, device, name):
     """Argument check: bf16 [T, heads, D] on this CUDA device whose heads of a token are contiguous; its token stride."""
     import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != D or t.device != device or (
-            t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D))):
-        raise ValueError(f"{name}: expected bfloat16 [T, heads, {D}] on {device} with contiguous heads, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
-    # the stride between tokens is of no account where there are not two
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    if t.dtype == torch.bfloat16 and t.device == device and t.dim() == 3:
+        n, h, d = t.shape
+        token, head, element = t.stride()
+        if d == D and (element == 1 and (head == D or h == 1) or n == 0 or h == 0):
+            # the stride between tokens is of no account where there are not two
+            return token if n > 1 else h * D
+    raise ValueError(f"{name}: expected bfloat16 [T, heads, {D}] on {device} with contiguous heads, got {t.dtype} "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _int_tensors(device, *sizes):
+    """int32 tensors of these sizes on 16-byte boundaries, cut from one allocation."""
+    import torch
+    cuts = [c for n in sizes for c in ((n, -n % 4) if n % 4 else (n,))]
+    parts = iter(torch.empty(sum(cuts), dtype=torch.int32, device=device).split_with_sizes(cuts))
+    out = []
+    for n in sizes:
+        out.append(next(parts))
+        if n % 4:
+            next(parts)
+    return out
 
 
 class _On:
     """The device of a call's tensors and the stream it runs on, both current inside ``with``."""
+
+    __slots__ = ("_raw", "_ctx")
 
     def __init__(self, device, stream):
         import torch
@@ -517,16 +534,17 @@ class _On:
             raise ValueError(f"expected CUDA tensors, got {device}")
         if stream is not None and stream.device != device:
             raise ValueError(f"stream of {stream.device} for tensors on {device}")
-        own = torch.cuda.current_stream(device)
-        self.stream = own if stream is None else stream
+        # the current stream's handle: a stream object for it costs more than a launch
+        own = torch._C._cuda_getCurrentRawStream(device.index)
+        self._raw = own if stream is None else stream.cuda_stream
         # the common case, all of it current already, enters nothing
-        self._ctx = (None if self.stream == own and torch.cuda.current_device() == device.index else
-                     torch.cuda.stream(self.stream))
+        self._ctx = (None if self._raw == own and torch.cuda.current_device() == device.index else
+                     torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream))
 
     def __enter__(self):
         if self._ctx is not None:
             self._ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        return self._raw
 
     def __exit__(self, *exc):
         if self._ctx is not None:
@@ -580,8 +598,8 @@ class KvCache:
         self.fmt = KV_MXFP4 if fp4 else KV_BF16
         self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, ps, D
         self.device = k.device
-        self.struct = KvCacheStruct(ctypes.sizeof(KvCacheStruct), self.fmt, pages, ps, heads, D, _ptr(k), _ptr(v),
-                                    _ptr(k_scale), _ptr(v_scale))
+        self.struct = KvCacheStruct(ctypes.sizeof(KvCacheStruct), self.fmt, pages, ps, heads, D, k.data_ptr(), v.data_ptr(),
+                                    k_scale.data_ptr() if fp4 else None, v_scale.data_ptr() if fp4 else None)
         data, scale = ctypes.c_size_t(), ctypes.c_size_t()
         _check(lib().moe_mxfp4_kv_cache_bytes(ctypes.byref(self.struct), ctypes.byref(data), ctypes.byref(scale)),
                "moe_mxfp4_kv_cache_bytes")
@@ -603,26 +621,27 @@ def cache_plan(ctx_lens, new_lens, block_table, held, free_ring, free_state, *, 
     i32, dev = torch.int32, block_table.device
     B, W = block_table.shape
     N = free_ring.numel()
+    given = [(ctx_lens, (B,), "ctx_lens"), (new_lens, (B,), "new_lens"), (held, (B,), "held"),
+             (block_table, (B, W), "block_table"), (free_ring, (N,), "free_ring"), (free_state, (2,), "free_state")]
+    if held_out is not None:
+        given.append((held_out, (B,), "held_out"))
+    if free_out is not None:
+        given.append((free_out, (2,), "free_out"))
+    if out is not None:
+        given += [(out.cu_q, (B + 1,), "cu_q"), (out.kv_lens, (B,), "kv_lens"), (out.slots, (num_tokens,), "slots"),
+                  (out.positions, (num_tokens,), "positions"), (out.refused, (1,), "refused"),
+                  (out.held, (B,), "held_out"), (out.free_state, (2,), "free_out")]
+    for t, shape, name in given:
+        _like(t, i32, shape, dev, name)
     with _On(dev, stream) as st:
         if out is None:
-            out = CachePlan(torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
-                            torch.empty(num_tokens, dtype=i32, device=dev),
-                            torch.empty(num_tokens, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev),
-                            torch.empty(B, dtype=i32, device=dev) if held_out is None else held_out,
-                            torch.empty(2, dtype=i32, device=dev) if free_out is None else free_out)
-        elif held_out is not None or free_out is not None:
+            out = CachePlan(*_int_tensors(dev, B + 1, B, num_tokens, num_tokens, 1, B, 2))
+        if held_out is not None or free_out is not None:
             out = out._replace(**{n: t for n, t in (("held", held_out), ("free_state", free_out)) if t is not None})
-        for t, shape, name in ((ctx_lens, (B,), "ctx_lens"), (new_lens, (B,), "new_lens"), (held, (B,), "held"),
-                               (block_table, (B, W), "block_table"), (free_ring, (N,), "free_ring"),
-                               (free_state, (2,), "free_state"), (out.cu_q, (B + 1,), "cu_q"),
-                               (out.kv_lens, (B,), "kv_lens"), (out.slots, (num_tokens,), "slots"),
-                               (out.positions, (num_tokens,), "positions"), (out.refused, (1,), "refused"),
-                               (out.held, (B,), "held_out"), (out.free_state, (2,), "free_out")):
-            _like(t, i32, shape, dev, name)
-        args = PlanArgs(ctypes.sizeof(PlanArgs), B, num_tokens, W, page_size, N,
-                        *[t.data_ptr() for t in (ctx_lens, new_lens, block_table, held, out.held, free_ring,
-                                                 free_state, out.free_state, out.cu_q, out.kv_lens, out.slots,
-                                                 out.positions, out.refused)])
+        args = PlanArgs(ctypes.sizeof(PlanArgs), B, num_tokens, W, page_size, N, ctx_lens.data_ptr(), new_lens.data_ptr(),
+                        block_table.data_ptr(), held.data_ptr(), out.held.data_ptr(), free_ring.data_ptr(),
+                        free_state.data_ptr(), out.free_state.data_ptr(), out.cu_q.data_ptr(), out.kv_lens.data_ptr(),
+                        out.slots.data_ptr(), out.positions.data_ptr(), out.refused.data_ptr())
         _check(lib().moe_mxfp4_cache_plan(ctypes.byref(args), st), "moe_mxfp4_cache_plan")
     return out
 
@@ -683,7 +702,7 @@ def kv_read(cache: KvCache, slots, stream=None):
     n, dev = slots.numel(), cache.device
     _like(slots, torch.int32, (n,), dev, "slots")
     with _On(dev, stream) as st:
-        k, v = (torch.empty((n, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=dev) for _ in range(2))
+        k, v = torch.empty((2, n, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=dev).unbind()
         _check(lib().moe_mxfp4_kv_read(ctypes.byref(cache.struct), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
                                        st), "moe_mxfp4_kv_read")
     return k, v
@@ -724,8 +743,11 @@ def attention(q, cache: KvCache, block_table, cu_q, kv_lens, *, max_q: int, max_
             workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
         elif workspace.device != dev:
             raise ValueError(f"workspace on {workspace.device}, q on {dev}")
-        _check(L.moe_mxfp4_attention(a, c, _ptr(workspace), 0 if workspace is None else workspace.numel() *
-                                     workspace.element_size(), st), "moe_mxfp4_attention")
+        if workspace is None:
+            status = L.moe_mxfp4_attention(a, c, None, 0, st)
+        else:
+            status = L.moe_mxfp4_attention(a, c, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
+        _check(status, "moe_mxfp4_attention")
     return out
 
 
