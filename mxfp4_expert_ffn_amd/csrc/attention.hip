@@ -185,6 +185,13 @@ __device__ __forceinline__ void lds_dma4(const uint8_t* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m), "v"(src) : "memory");
 }
 
+// Of a bf16 tile that waves share, chunk c of value row r is stored at c ^ this:
+// a transposing read takes two neighbouring chunks of rows 8 g + k, k = 0..3,
+// of all four g at once, and finds them in twice all banks.
+__device__ constexpr int value_swizzle(int D, int r) {
+    return D == 128 ? 2 * (r % 4 + 4 * (r / 8 % 2)) : 2 * (r % 4 / 2 + 2 * (r / 8 % 2));
+}
+
 // Starts the loads of a tile into its slot dst (an LDS address, the same for
 // all lanes); of WAVES waves that share the tile, the `part`-th of them starts
 // its share.  What this wave read from the slot before has arrived.
@@ -230,7 +237,9 @@ __device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pag
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (WAVES > 1 && part != i * WAVES / N) continue;
-            lds_dma16<ONCE>(a.v + (i < 16 / R ? b0 : b1) * (2 * D) + i % (16 / R) * 1024, lane * 16, dst + T::kValues + i * 1024);
+            const int row = i * R + lane / C;      // where waves share it: chunk c at c ^ value_swizzle
+            const int off = WAVES > 1 ? lane / C * (2 * D) + ((lane % C) ^ value_swizzle(D, row)) * 16 : lane * 16;
+            lds_dma16<ONCE>(a.v + (i < 16 / R ? b0 : b1) * (2 * D) + i % (16 / R) * 1024, off, dst + T::kValues + i * 1024);
         }
     }
 }
@@ -457,27 +466,70 @@ template <int D> struct SharedTile {
     static constexpr int kBytes = (2 * (D / 32) + D / 16) * 1024;
     __device__ __forceinline__ bf16x8_t at(int i) const { return *reinterpret_cast<const bf16x8_t*>(f + i * 1024); }
     __device__ __forceinline__ bf16x8_t key(int t, int s) const { return at(t * (D / 32) + s); }
+    __device__ __forceinline__ bf16x8_t value(int n) const { return at(2 * (D / 32) + n); }
+};
+
+// A bf16 tile needs no decoding, so the waves along the rows read it as
+// fetched: rows of keys are operands as they stand, rows of values become
+// operands by the LDS's transposing reads.  Its tile n holds elements 16 n ..
+// 16 n + 15 in order.
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef const __attribute__((address_space(3))) uint8_t* LdsBytes;
+template <int D> struct DirectTile {
+    LdsBytes k[2], v;                              // this lane's key rows, and where its first transposing read begins
+    int m;
+    __device__ __forceinline__ DirectTile(LdsBytes tile, int lane) : m(lane % 16) {
+        const int g = lane / 16, row = 8 * g + m / 4;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) k[t] = tile + (8 * (m / 4) + 4 * t + m % 4) * (2 * D);
+        v = tile + Tile<MOE_KV_BF16, D>::kValues + row * (2 * D) + ((m % 4 / 2) ^ value_swizzle(D, row)) * 16 + m % 2 * 8;
+        m = ((lane / 16) * (D / 32)) ^ (m % (D / 8));
+    }
+    __device__ __forceinline__ bf16x8_t key(int t, int s) const {
+        return *reinterpret_cast<const __attribute__((address_space(3))) bf16x8_t*>(k[t] + (m ^ s) * 16);
+    }
+    __device__ __forceinline__ bf16x8_t value(int n) const {
+        // bits 5 and up of the address select the pair of chunks within a row
+        LdsBytes p = (LdsBytes)((uint32_t)(uintptr_t)v ^ (uint32_t)(32 * n));
+        const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+        const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * (2 * D)));
+        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// Such tiles for attend_part.
+template <int D, typename Tile_> struct Masked : Tile_ {
+    using Tile_::Tile_;
+    __device__ __forceinline__ Masked(const Tile_& t) : Tile_(t) {}
     template <typename F> __device__ __forceinline__ void values(uint32_t keep, F f) const {
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) {
-            u32x4_t w = __builtin_bit_cast(u32x4_t, at(2 * (D / 32) + n));
+            u32x4_t w = __builtin_bit_cast(u32x4_t, this->value(n));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 w[i] &= ((keep >> (2 * i)) & 1 ? 0xFFFFu : 0u) | ((keep >> (2 * i + 1)) & 1 ? 0xFFFF0000u : 0u);
             f(n, __builtin_bit_cast(bf16x8_t, w));
         }
     }
-    __device__ __forceinline__ bool wild(uint32_t) const {
+    // whether one of the lane group's live keys has an infinite or NaN value
+    __device__ __forceinline__ bool wild(uint32_t live) const {
         bool x = false;
         for (int n = 0; n < D / 16; ++n) {
-            const u32x4_t w = __builtin_bit_cast(u32x4_t, at(2 * (D / 32) + n));
+            const u32x4_t w = __builtin_bit_cast(u32x4_t, this->value(n));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+            for (int i = 0; i < 4; ++i)
+                x |= ((live >> (2 * i)) & 1 && (w[i] & 0x7F80u) == 0x7F80u) ||
+                     ((live >> (2 * i + 1)) & 1 && (w[i] & 0x7F800000u) == 0x7F800000u);
         }
         return x;
     }
     __device__ __forceinline__ void anew() {}
 };
+
+// After a loop that is left from its middle too: keeps the compiler from telling
+// the ways out apart.  Of a loop with several exits it would carry all sums,
+// as before the tile and as after, to one common end: twice the registers.
+__device__ __forceinline__ void one_exit(int& x, int& y) { asm volatile("" : "+s"(x), "+s"(y)); }
 
 __device__ __forceinline__ void pin() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -502,23 +554,28 @@ __device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const Src& src, 
     return true;
 }
 
-// The same of a shared tile, all of a product's operands asked for before its
-// first: read one by one, each would wait for LDS longer than its MT matrix
-// instructions last.  The values' reads pass under the softmax.
-template <int D, int MT>
-__device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const SharedTile<D>& src, const bf16x8_t (&qf)[MT][D / 32],
-                                             float c) {
+// The same of a shared tile, operands asked for kAhead steps before their
+// product: read on use, each would wait for LDS longer than its MT matrix
+// instructions last.  The first values' reads pass under the softmax.
+constexpr int kAhead = 4;
+template <int D, int MT, typename Src>
+__device__ __forceinline__ bool attend_shared(Sums<D, MT>& sums, const Src& src, const bf16x8_t (&qf)[MT][D / 32], float c) {
     constexpr int KS = D / 32, NT = D / 16;
-    bf16x8_t kf[2 * KS], vf[NT];
-#pragma unroll
-    for (int i = 0; i < 2 * KS; ++i) kf[i] = src.at(i);
-    pin();
+    bf16x8_t x[kAhead];
     f32x4_t sc[MT][2];
-    scores<D, MT>(sc, [&](int t, int s) { return kf[t * KS + s]; }, qf);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = src.key(i / KS, i % KS);
     pin();
 #pragma unroll
-    for (int n = 0; n < NT; ++n) vf[n] = src.at(2 * KS + n);
-    pin();
+    for (int i = 0; i < 2 * KS; ++i) {
+        const int t = i / KS, s = i % KS;
+#pragma unroll
+        for (int q = 0; q < MT; ++q) sc[q][t] = mfma(x[i % kAhead], qf[q][s], s == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : sc[q][t]);
+        const int next = i + kAhead;
+        if (next < 2 * KS) x[i % kAhead] = src.key(next / KS, next % KS);
+        else x[i % kAhead] = src.value(next - 2 * KS);
+        pin();
+    }
     float top[MT];
     tops<MT>(top, sc, c);
     bool move = false;
@@ -528,9 +585,12 @@ __device__ __forceinline__ bool attend_whole(Sums<D, MT>& sums, const SharedTile
     bf16x8_t pf[MT];
     weights<D, MT>(sums, pf, sc, c);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int q = 0; q < MT; ++q) sums.o[q][n] = mfma(vf[n], pf[q], sums.o[q][n]);
+        for (int q = 0; q < MT; ++q) sums.o[q][n] = mfma(x[n % kAhead], pf[q], sums.o[q][n]);
+        if (n + kAhead < NT) x[n % kAhead] = src.value(n + kAhead);
+        pin();
+    }
     return true;
 }
 
@@ -687,7 +747,9 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
     constexpr bool SHARED = WR == kWaves;          // or by all four, at the same time
     using T = Tile<FMT, D>;
     typedef float JoinRows[kWaves][16][D + 4];
-    constexpr int kRing = SHARED ? 0 : 2 * T::kBytes, kTiles = SHARED ? 2 * (SharedTile<D>::kBytes + T::kBytes) : kWaves * kRing;
+    constexpr bool DIRECT = SHARED && FMT == MOE_KV_BF16;      // as fetched
+    constexpr int kRing = SHARED ? 0 : 2 * T::kBytes;
+    constexpr int kTiles = DIRECT ? 3 * T::kBytes : SHARED ? 2 * (SharedTile<D>::kBytes + T::kBytes) : kWaves * kRing;
     constexpr int kLds = kTiles > (int)sizeof(JoinRows) ? kTiles : sizeof(JoinRows);
     __shared__ __align__(1024) uint8_t lds[kLds];
     __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
@@ -802,17 +864,13 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
         c1 = complete ? rg.total : min(c1, rg.total);
         const int rw = r0 + 16 * MT * wr;          // this wave's first row
 
-        // queries and views of this lane's row in each 16-row tile
+        // queries of this lane's row in each 16-row tile
         bf16x8_t qf[MT][KS];
-        View vw[MT];
 #pragma unroll
         for (int q = 0; q < MT; ++q) {
             const int r = rw + 16 * q + m;
             const bool in = r < rows;
             const int tok = in ? r / a.G : 0, h = in ? hk * a.G + r % a.G : 0;
-            const int p = sq.kv - sq.n + tok;
-            vw[q].up = !in || p < 0 ? 0 : a.causal ? min(p + 1, sq.kv) : sq.kv;
-            vw[q].lo = a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
             const uint16_t* src = a.q + (int64_t)(sq.start + tok) * a.qs + (int64_t)h * D + g * (D / 4);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
@@ -821,6 +879,18 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 qf[q][s] = __builtin_bit_cast(bf16x8_t, x);
             }
         }
+        // what they see; found anew for each tile that needs it, since kept it
+        // would cost the common tiles registers
+        auto views = [&](View (&vw)[MT]) {
+            int first = rw + m;
+            asm volatile("" : "+v"(first));
+#pragma unroll
+            for (int q = 0; q < MT; ++q) {
+                const int r = first + 16 * q, p = sq.kv - sq.n + (int)((unsigned)r / (unsigned)a.G);
+                vw[q].up = r >= rows || p < 0 ? 0 : a.causal ? min(p + 1, sq.kv) : sq.kv;
+                vw[q].lo = a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
+            }
+        };
         // keys that every row of this wave sees, [all_lo, all_up) and below
         // sinks, and that any of them does (a wave without rows: none)
         const int pw0 = sq.kv - sq.n + min(rw, rows - 1) / a.G;
@@ -852,14 +922,15 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
         };
         if constexpr (SHARED) {
             // The waves along the rows share every tile.  Between two barriers
-            // they start the loads of the tile after the next, turn the next one,
-            // which has arrived, into operands, and read this one's.
+            // they start the loads of the tile after the next and read this one;
+            // MXFP4: and turn the next one, which has arrived, into operands.
             const int any_up = rw >= rows || pw1 < 0 ? 0 : a.causal ? min(pw1 + 1, sq.kv) : sq.kv;
             const int any_lo = a.window > 0 ? (int)max((int64_t)pw0 - a.window + 1, (int64_t)0) : 0;
             auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
             auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
-            uint8_t* const raws = lds + 2 * SharedTile<D>::kBytes;
-            const uint32_t raw_at = lds_at + 2 * SharedTile<D>::kBytes;
+            constexpr int kRaws = DIRECT ? 0 : 2 * SharedTile<D>::kBytes;
+            uint8_t* const raws = lds + kRaws;
+            const uint32_t raw_at = lds_at + kRaws;
             auto turn = [&](int slot, const Pages& p, int tile) {
                 const int key0 = tile * kTile;
                 const bool all = in_cache(a, p.a) && in_cache(a, p.b) && key0 + kTile <= sq.kv;
@@ -873,41 +944,56 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 pg2 = pages_for(c + 2);
                 fetch<FMT, D, kWaves, false>(raw_at, a, pg0, tile_for(c), hk, lane, wave);
                 fetch<FMT, D, kWaves, false>(raw_at + T::kBytes, a, pg1, tile_for(c + 1), hk, lane, wave);
-                wait_loads<0>();
-                lds_barrier();
-                turn(0, pg0, tile_for(c));
+                if constexpr (!DIRECT) {
+                    wait_loads<0>();
+                    lds_barrier();
+                    turn(0, pg0, tile_for(c));
+                }
             }
             auto share = [&] {
-                wait_loads<0>();                   // tile c + 1 has arrived, this wave's part of it
-                lds_barrier();                     // and the others'; tile c is operands, c - 1 read
-                fetch<FMT, D, kWaves, false>(raw_at + buf * T::kBytes, a, pg2, tile_for(c + 2), hk, lane, wave);
-                turn(buf ^ 1, pg1, tile_for(c + 1));
+                if constexpr (DIRECT) {
+                    wait_loads<T::kFetches / kWaves>();        // tile c has arrived, this wave's part of it
+                    lds_barrier();                 // and the others'; tile c - 1 is read
+                    fetch<FMT, D, kWaves, false>(raw_at + (buf == 0 ? 2 : buf - 1) * T::kBytes, a, pg2, tile_for(c + 2), hk, lane, wave);
+                } else {
+                    wait_loads<0>();               // tile c + 1 has arrived, this wave's part of it
+                    lds_barrier();                 // and the others'; tile c is operands, c - 1 read
+                    fetch<FMT, D, kWaves, false>(raw_at + buf * T::kBytes, a, pg2, tile_for(c + 2), hk, lane, wave);
+                    turn(buf ^ 1, pg1, tile_for(c + 1));
+                }
             };
             auto next = [&] {
                 ++c;
-                buf ^= 1;
+                if constexpr (DIRECT) buf = buf == 2 ? 0 : buf + 1;
+                else buf ^= 1;
                 pg0 = pg1;
                 pg1 = pg2;
                 pg2 = pages_for(c + 2);
             };
+            auto tile_here = [&] {
+                if constexpr (DIRECT) return DirectTile<D>((LdsBytes)(lds_void*)lds + buf * T::kBytes, lane);
+                else return SharedTile<D>{lds + buf * SharedTile<D>::kBytes + lane * 16};
+            };
             while (c < c1) {
-                bool shared = false;
-                while (c < c1 && whole_at(tile_at(c) * kTile, pg0)) {
+                int shared = 0;
+                while (__builtin_expect(c < c1 && whole_at(tile_at(c) * kTile, pg0), 1)) {
                     share();
-                    const SharedTile<D> tile{lds + buf * SharedTile<D>::kBytes + lane * 16};
-                    if (!attend_whole<D, MT>(sums, tile, qf, a.c)) {
-                        shared = true;
+                    if (__builtin_expect(!attend_shared<D, MT>(sums, tile_here(), qf, a.c), 0)) {
+                        shared = 1;
                         break;
                     }
                     next();
                 }
+                one_exit(c, shared);
                 if (c >= c1) break;
                 if (!shared) share();
                 const int key0 = tile_at(c) * kTile;
                 if (key0 < any_up && (key0 + kTile > any_lo || key0 < a.sinks)) {
-                    const SharedTile<D> tile{lds + buf * SharedTile<D>::kBytes + lane * 16};
+                    const Masked<D, decltype(tile_here())> tile(tile_here());
                     const uint32_t live = live_at(key0, pg0);
-                    if (!whole_at(key0, pg0) && __any(tile.wild(live)))
+                    View vw[MT];
+                    views(vw);
+                    if (__builtin_expect(!whole_at(key0, pg0) && __any(tile.wild(live)), 0))
                         attend_part<D, MT, true>(sums, tile, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
                     else
                         attend_part<D, MT, false>(sums, tile, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
@@ -962,6 +1048,8 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                     if (!attend_whole<D, MT>(sums, RawTile<FMT, D>(base + at, lane), qf, a.c)) break;
                     advance();
                 }
+                int same = 0;
+                one_exit(c, same);
                 if (c >= c1) break;
                 // any tile
                 wait_loads<kUnder>();
@@ -969,7 +1057,11 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 const RawTile<FMT, D> r(base + at, lane);
                 const uint32_t live = live_at(key0, pg0);
                 if (!whole_at(key0, pg0) && __any(r.wild(live))) wild = true;
-                else attend_part<D, MT, false>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                else {
+                    View vw[MT];
+                    views(vw);
+                    attend_part<D, MT, false>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                }
                 advance();
             }
             // tiles put off: those that rows see in part and that hold an infinite
@@ -985,6 +1077,8 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                     wait_loads<0>();
                     const RawTile<FMT, D> r(base, lane);
                     const uint32_t live = live_at(key0, pc);
+                    View vw[MT];
+                    views(vw);
                     if (__any(r.wild(live)))
                         attend_part<D, MT, true>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
                 }
@@ -1001,12 +1095,17 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 sh_l[wave][m] = sums.l[q][0];
             }
             float* row = sh_o[wave][m];
+            if constexpr (DIRECT) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4_t*>(row + 16 * n + 4 * g) = sums.o[q][n];
+            } else {
 #pragma unroll
-                for (int n = 0; n < NT; n += 4)
-                    *reinterpret_cast<f32x4_t*>(row + (4 * g + i) * NT + n) =
-                        f32x4_t{sums.o[q][n][i], sums.o[q][n + 1][i], sums.o[q][n + 2][i], sums.o[q][n + 3][i]};
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < NT; n += 4)
+                        *reinterpret_cast<f32x4_t*>(row + (4 * g + i) * NT + n) =
+                            f32x4_t{sums.o[q][n][i], sums.o[q][n + 1][i], sums.o[q][n + 2][i], sums.o[q][n + 3][i]};
+            }
             __syncthreads();
             const int wj = tid / TPR / 16, rr = tid / TPR % 16, d0 = tid % TPR * E;
             const int r = r0 + 16 * MT * wj + 16 * q + rr;
