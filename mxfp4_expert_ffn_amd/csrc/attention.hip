@@ -141,15 +141,17 @@ __device__ __forceinline__ void load_words(uint32_t* dst, const uint8_t* src) {
     }
 }
 
-// Block table entries of a tile's two halves of 16 keys, as they stand.  They
-// are read through the scalar cache, and looked at only where they are used,
-// a tile or more later, so that nothing waits for them.
+// A tile and the block table entries of its two halves of 16 keys, as they
+// stand.  They are read through the scalar cache, and looked at only where they
+// are used, a tile or more later, so that nothing waits for them.
 struct Pages {
-    int a, b;
+    int tile, a, b;
 };
-__device__ __forceinline__ Pages pages_of(const AttnArgs& a, ScalarInts row, int tile, int kv) {
-    const int key = tile * kTile;                  // below kv, which is within max_blocks pages
-    return Pages{row[key >> a.shift], row[min(key + 16, kv - 1) >> a.shift]};
+// row: the sequence's entries; last: its last key's
+__device__ __forceinline__ Pages pages_of(const AttnArgs& a, ScalarInts row, int tile, int last) {
+    const int first = (tile * kTile) >> a.shift, second = min(first + (a.shift == 4), last);
+    typedef const __attribute__((address_space(4))) uint8_t* Bytes;
+    return Pages{tile, *(ScalarInts)((Bytes)row + (uint32_t)(4 * first)), *(ScalarInts)((Bytes)row + (uint32_t)(4 * second))};
 }
 __device__ __forceinline__ bool in_cache(const AttnArgs& a, int page) { return (unsigned)page < (unsigned)a.num_pages; }
 
@@ -185,6 +187,22 @@ __device__ __forceinline__ void lds_dma4(const uint8_t* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(m), "v"(src) : "memory");
 }
 
+// The first LANES lanes' only, of all 64 that are active here.
+template <int LANES, int BYTES>
+__device__ __forceinline__ void lds_dma_low(const uint8_t* base, uint32_t off, uint32_t lds) {
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    const uint64_t s = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(b >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)b);
+    const uint32_t m = __builtin_amdgcn_readfirstlane((int)lds);
+    const uint64_t on = ((uint64_t)1 << LANES) - 1;
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
+                     ::"s"(m), "v"(off), "s"(s), "s"(on) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, %3\n\tglobal_load_lds_dword %1, %2\n\ts_mov_b64 exec, -1"
+                     ::"s"(m), "v"(off), "s"(s), "s"(on) : "memory");
+}
+
 // Of a bf16 tile that waves share, chunk c of value row r is stored at c ^ this:
 // a transposing read takes two neighbouring chunks of rows 8 g + k, k = 0..3,
 // of all four g at once, and finds them in twice all banks.
@@ -192,54 +210,83 @@ __device__ constexpr int value_swizzle(int D, int r) {
     return D == 128 ? 2 * (r % 4 + 4 * (r / 8 % 2)) : 2 * (r % 4 / 2 + 2 * (r / 8 % 2));
 }
 
+// First row of a half tile's keys in the cache; page 0 stands in for none: read,
+// then not used.
+__device__ __forceinline__ int64_t half_row(const AttnArgs& a, int page, int key, int hk) {
+    return (((int64_t)(in_cache(a, page) ? page : 0) * a.Hk + hk) << a.shift) + (key & ((1 << a.shift) - 1));
+}
+
 // Starts the loads of a tile into its slot dst (an LDS address, the same for
-// all lanes); of WAVES waves that share the tile, the `part`-th of them starts
-// its share.  What this wave read from the slot before has arrived.
-template <int FMT, int D, int WAVES, bool ONCE>
-__device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pages& pg, int tile, int hk, int lane, int part) {
+// all lanes).  What this wave read from the slot before has arrived.
+template <int FMT, int D, bool ONCE>
+__device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pages& pg, int hk, int lane) {
     using T = Tile<FMT, D>;
-    const int mask = (1 << a.shift) - 1;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    // first row of each half; page 0 stands in for none: read, then not used
-    const int64_t b0 = (((int64_t)(in_cache(a, pg.a) ? pg.a : 0) * a.Hk + hk) << a.shift) + ((tile * kTile) & mask);
-    const int64_t b1 = (((int64_t)(in_cache(a, pg.b) ? pg.b : 0) * a.Hk + hk) << a.shift) + ((tile * kTile + 16) & mask);
+    const int64_t b0 = half_row(a, pg.a, pg.tile * kTile, hk), b1 = half_row(a, pg.b, pg.tile * kTile + 16, hk);
     if constexpr (FMT == MOE_KV_MXFP4 && D == 128) {
         // chunk c of row r is stored at c ^ (r / 8)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (WAVES == 1 || part == h)
-                lds_dma16<ONCE>(a.k + (h ? b1 : b0) * 64, lane / 4 * 64 + ((lane % 4) ^ (2 * h + lane / 32)) * 16, dst + h * 1024);
+            lds_dma16<ONCE>(a.k + (h ? b1 : b0) * 64, lane / 4 * 64 + ((lane % 4) ^ (2 * h + lane / 32)) * 16, dst + h * 1024);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (WAVES == 1 || part == 2 + h) lds_dma16<ONCE>(a.v + (h ? b1 : b0) * 64, lane * 16, dst + T::kValues + h * 1024);
-        if (WAVES == 1 || part == 3) {
-            const uint8_t* sc = lane < 32 ? a.ks : a.vs;
-            lds_dma4(sc + (lane & 16 ? b1 : b0) * 4 + lane % 16 * 4, dst + T::kScales);
-        }
+        for (int h = 0; h < 2; ++h) lds_dma16<ONCE>(a.v + (h ? b1 : b0) * 64, lane * 16, dst + T::kValues + h * 1024);
+        const uint8_t* sc = lane < 32 ? a.ks : a.vs;
+        lds_dma4(sc + (lane & 16 ? b1 : b0) * 4 + lane % 16 * 4, dst + T::kScales);
     } else if constexpr (FMT == MOE_KV_MXFP4) {
         const int64_t base = lane < 32 ? b0 : b1;
         const int chunk = (lane % 2) ^ ((lane / 16) & 1);               // chunk c of row r at c ^ (r / 8 mod 2)
-        if (WAVES == 1 || part == 0) lds_dma16(a.k + base * 32 + (lane / 2 % 16 * 32 + chunk * 16), dst);
-        if (WAVES == 1 || part == 1) lds_dma16(a.v + base * 32 + lane % 32 * 16, dst + T::kValues);
-        if (WAVES == 1 || part == 2) {
-            const uint8_t* sc = lane & 16 ? a.vs : a.ks;                // lanes 32.. repeat lanes 0..31
-            lds_dma4(sc + (lane & 8 ? b1 : b0) * 2 + lane % 8 * 4, dst + T::kScales);
-        }
+        lds_dma16(a.k + base * 32 + (lane / 2 % 16 * 32 + chunk * 16), dst);
+        lds_dma16(a.v + base * 32 + lane % 32 * 16, dst + T::kValues);
+        const uint8_t* sc = lane & 16 ? a.vs : a.ks;                    // lanes 32.. repeat lanes 0..31
+        lds_dma4(sc + (lane & 8 ? b1 : b0) * 2 + lane % 8 * 4, dst + T::kScales);
     } else {
         constexpr int C = D / 8, R = 64 / C, N = kTile / R;             // chunks per row, rows per load, loads
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (WAVES > 1 && part != i * WAVES / N) continue;
             // chunk c of row r at c ^ (its lane m = 4 (r / 8) + r mod 4)
             const int row = i * R + lane / C, mm = 4 * (row / 8) + row % 4;
             lds_dma16<ONCE>(a.k + (i < 16 / R ? b0 : b1) * (2 * D), row % 16 * (2 * D) + ((lane % C) ^ (mm % C)) * 16, dst + i * 1024);
         }
 #pragma unroll
+        for (int i = 0; i < N; ++i)
+            lds_dma16<ONCE>(a.v + (i < 16 / R ? b0 : b1) * (2 * D) + i % (16 / R) * 1024, lane * 16, dst + T::kValues + i * 1024);
+    }
+}
+
+// The same where the workgroup's four waves share the tile: wave `part` starts
+// its loads, each of one half.
+template <int FMT, int D>
+__device__ __forceinline__ void fetch_part(uint32_t dst, const AttnArgs& a, const Pages& pg, int hk, int lane, int part) {
+    using T = Tile<FMT, D>;
+    if constexpr (FMT == MOE_KV_MXFP4) {
+        const int h = part % 2;                    // keys or values of half h
+        const bool keys = part < 2;
+        const int64_t b = half_row(a, h ? pg.b : pg.a, pg.tile * kTile + 16 * h, hk);
+        const uint8_t* src = (keys ? a.k : a.v) + b * (D / 2);
+        const uint32_t to = dst + (keys ? 0 : T::kValues) + h * (8 * D);
+        if constexpr (D == 128) {
+            const int chunk = keys ? (lane % 4) ^ (2 * h + lane / 32) : lane % 4;
+            lds_dma16<false>(src, lane / 4 * 64 + chunk * 16, to);
+            lds_dma_low<16, 4>((keys ? a.ks : a.vs) + b * 4, lane * 4, dst + T::kScales + part * 64);
+        } else {
+            const int chunk = keys ? (lane % 2) ^ ((lane / 16) & 1) : lane % 2;
+            lds_dma_low<32, 16>(src, lane / 2 * 32 + chunk * 16, to);
+            lds_dma_low<8, 4>((keys ? a.ks : a.vs) + b * 2, lane * 4, dst + T::kScales + part * 32);
+        }
+    } else {
+        constexpr int C = D / 8, R = 64 / C, N = kTile / R / kWaves;    // chunks per row, rows per load, loads
+        const int h = part / 2;
+        const int64_t b = half_row(a, h ? pg.b : pg.a, pg.tile * kTile + 16 * h, hk);
+#pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (WAVES > 1 && part != i * WAVES / N) continue;
-            const int row = i * R + lane / C;      // where waves share it: chunk c at c ^ value_swizzle
-            const int off = WAVES > 1 ? lane / C * (2 * D) + ((lane % C) ^ value_swizzle(D, row)) * 16 : lane * 16;
-            lds_dma16<ONCE>(a.v + (i < 16 / R ? b0 : b1) * (2 * D) + i % (16 / R) * 1024, off, dst + T::kValues + i * 1024);
+            const int row = (part * N + i) * R + lane / C, mm = 4 * (row / 8) + row % 4;
+            lds_dma16<false>(a.k + b * (2 * D), row % 16 * (2 * D) + ((lane % C) ^ (mm % C)) * 16, dst + (part * N + i) * 1024);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int row = (part * N + i) * R + lane / C;              // chunk c at c ^ value_swizzle
+            lds_dma16<false>(a.v + b * (2 * D), row % 16 * (2 * D) + ((lane % C) ^ value_swizzle(D, row)) * 16,
+                             dst + T::kValues + (part * N + i) * 1024);
         }
     }
 }
@@ -849,8 +896,8 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             unit += c1 - c0;
         } else {
             const int in = (int)(blockIdx.x % (unsigned)(a.row_tiles * a.Hk));
-            hk = in / a.row_tiles;
-            set = in % a.row_tiles + (int)(unit - blockIdx.x);
+            hk = in % a.Hk;                        // sets of one head on one XCD, where it has a multiple of 8
+            set = in / a.Hk + (int)(unit - blockIdx.x);
             if ((int64_t)set * ROWS >= rows) return;
             c0 = 0;
             c1 = INT32_MAX;
@@ -897,6 +944,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
         const int pw1 = sq.kv - sq.n + (min(rw + 16 * MT, rows) - 1) / a.G;
         const int all_up = pw0 < 0 ? 0 : a.causal ? min(pw0 + 1, sq.kv) : sq.kv;
         const int all_lo = a.window > 0 ? (int)max((int64_t)pw1 - a.window + 1, (int64_t)0) : 0;
+        const int last_page = (sq.kv - 1) >> a.shift;
 
         Sums<D, MT> sums;
 #pragma unroll
@@ -910,15 +958,17 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
 
         // tiles c0 + wk, c0 + wk + WK, ...
         auto tile_at = [&](int x) { return x < rg.head ? x : rg.lo + x - rg.head; };
+        auto pages_for = [&](int x) { return pages_of(a, trow, tile_at(min(x, c1 - 1)), last_page); };
         // A tile that every row sees whole needs no mask.  Else keys in no page
         // or behind the last are dead (their values count as 0) and the others
         // are masked row by row.
-        auto whole_at = [&](int key0, const Pages& p) {
-            return in_cache(a, p.a) && in_cache(a, p.b) && key0 + kTile <= all_up && (key0 >= all_lo || key0 + kTile <= a.sinks);
+        const int whole_up = all_up / kTile, whole_lo = all_lo / kTile + (all_lo % kTile != 0), whole_sinks = a.sinks / kTile;
+        auto whole = [&](const Pages& p) {
+            return in_cache(a, p.a) && in_cache(a, p.b) && p.tile < whole_up && (p.tile >= whole_lo || p.tile < whole_sinks);
         };
-        auto live_at = [&](int key0, const Pages& p) {
+        auto live_in = [&](const Pages& p) {
             const bool ok0 = in_cache(a, p.a), ok1 = in_cache(a, p.b);
-            return (g < 2 ? ok0 : ok1) ? low_bits(sq.kv - key0 - 8 * g) : 0u;
+            return (g < 2 ? ok0 : ok1) ? low_bits(sq.kv - p.tile * kTile - 8 * g) : 0u;
         };
         if constexpr (SHARED) {
             // The waves along the rows share every tile.  Between two barriers
@@ -926,40 +976,40 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             // MXFP4: and turn the next one, which has arrived, into operands.
             const int any_up = rw >= rows || pw1 < 0 ? 0 : a.causal ? min(pw1 + 1, sq.kv) : sq.kv;
             const int any_lo = a.window > 0 ? (int)max((int64_t)pw0 - a.window + 1, (int64_t)0) : 0;
-            auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
-            auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
             constexpr int kRaws = DIRECT ? 0 : 2 * SharedTile<D>::kBytes;
             uint8_t* const raws = lds + kRaws;
             const uint32_t raw_at = lds_at + kRaws;
-            auto turn = [&](int slot, const Pages& p, int tile) {
-                const int key0 = tile * kTile;
-                const bool all = in_cache(a, p.a) && in_cache(a, p.b) && key0 + kTile <= sq.kv;
-                share_out<FMT, D>(raws + slot * T::kBytes, lds + slot * SharedTile<D>::kBytes, all ? 0u : live_at(key0, p), all, wave, lane);
+            auto turn = [&](int slot, const Pages& p) {
+                const bool all = in_cache(a, p.a) && in_cache(a, p.b) && p.tile < sq.kv / kTile;
+                share_out<FMT, D>(raws + slot * T::kBytes, lds + slot * SharedTile<D>::kBytes, all ? 0u : live_in(p), all, wave, lane);
             };
             int c = c0, buf = 0;                   // tile and its slot
             Pages pg0{}, pg1{}, pg2{};             // of tiles c, c + 1, c + 2
-            if (c < c1) {
+            auto begin = [&] {
+                c = c0;
+                buf = 0;
+                if (c >= c1) return;
                 pg0 = pages_for(c);
                 pg1 = pages_for(c + 1);
                 pg2 = pages_for(c + 2);
-                fetch<FMT, D, kWaves, false>(raw_at, a, pg0, tile_for(c), hk, lane, wave);
-                fetch<FMT, D, kWaves, false>(raw_at + T::kBytes, a, pg1, tile_for(c + 1), hk, lane, wave);
+                fetch_part<FMT, D>(raw_at, a, pg0, hk, lane, wave);
+                fetch_part<FMT, D>(raw_at + T::kBytes, a, pg1, hk, lane, wave);
                 if constexpr (!DIRECT) {
                     wait_loads<0>();
                     lds_barrier();
-                    turn(0, pg0, tile_for(c));
+                    turn(0, pg0);
                 }
-            }
+            };
             auto share = [&] {
                 if constexpr (DIRECT) {
                     wait_loads<T::kFetches / kWaves>();        // tile c has arrived, this wave's part of it
                     lds_barrier();                 // and the others'; tile c - 1 is read
-                    fetch<FMT, D, kWaves, false>(raw_at + (buf == 0 ? 2 : buf - 1) * T::kBytes, a, pg2, tile_for(c + 2), hk, lane, wave);
+                    fetch_part<FMT, D>(raw_at + (buf == 0 ? 2 : buf - 1) * T::kBytes, a, pg2, hk, lane, wave);
                 } else {
                     wait_loads<0>();               // tile c + 1 has arrived, this wave's part of it
                     lds_barrier();                 // and the others'; tile c is operands, c - 1 read
-                    fetch<FMT, D, kWaves, false>(raw_at + buf * T::kBytes, a, pg2, tile_for(c + 2), hk, lane, wave);
-                    turn(buf ^ 1, pg1, tile_for(c + 1));
+                    fetch_part<FMT, D>(raw_at + buf * T::kBytes, a, pg2, hk, lane, wave);
+                    turn(buf ^ 1, pg1);
                 }
             };
             auto next = [&] {
@@ -974,9 +1024,16 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 if constexpr (DIRECT) return DirectTile<D>((LdsBytes)(lds_void*)lds + buf * T::kBytes, lane);
                 else return SharedTile<D>{lds + buf * SharedTile<D>::kBytes + lane * 16};
             };
+            typedef Masked<D, decltype(tile_here())> Any;
+            auto seen_here = [&] {                 // by any row of this wave
+                const int key0 = pg0.tile * kTile;
+                return key0 < any_up && (key0 + kTile > any_lo || key0 < a.sinks);
+            };
+            int wild = 0;
+            begin();
             while (c < c1) {
                 int shared = 0;
-                while (__builtin_expect(c < c1 && whole_at(tile_at(c) * kTile, pg0), 1)) {
+                while (__builtin_expect(c < c1 && whole(pg0), 1)) {
                     share();
                     if (__builtin_expect(!attend_shared<D, MT>(sums, tile_here(), qf, a.c), 0)) {
                         shared = 1;
@@ -987,21 +1044,35 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 one_exit(c, shared);
                 if (c >= c1) break;
                 if (!shared) share();
-                const int key0 = tile_at(c) * kTile;
-                if (key0 < any_up && (key0 + kTile > any_lo || key0 < a.sinks)) {
-                    const Masked<D, decltype(tile_here())> tile(tile_here());
-                    const uint32_t live = live_at(key0, pg0);
-                    View vw[MT];
-                    views(vw);
-                    if (__builtin_expect(!whole_at(key0, pg0) && __any(tile.wild(live)), 0))
-                        attend_part<D, MT, true>(sums, tile, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
-                    else
-                        attend_part<D, MT, false>(sums, tile, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                if (seen_here()) {
+                    const Any tile(tile_here());
+                    const uint32_t live = live_in(pg0);
+                    if (!whole(pg0) && __any(tile.wild(live))) {
+                        wild = 1;
+                    } else {
+                        View vw[MT];
+                        views(vw);
+                        attend_part<D, MT, false>(sums, tile, qf, vw, pg0.tile * kTile + 8 * g, live, a.sinks, a.c);
+                    }
                 }
                 next();
             }
             wait_loads<0>();
-            lds_barrier();                         // the buffers are used again below
+            // tiles put off, as below; the waves go through them together
+            if (__syncthreads_or(wild)) {
+                for (begin(); c < c1; next()) {
+                    share();
+                    if (whole(pg0) || !seen_here()) continue;
+                    const Any tile(tile_here());
+                    const uint32_t live = live_in(pg0);
+                    View vw[MT];
+                    views(vw);
+                    if (__any(tile.wild(live)))
+                        attend_part<D, MT, true>(sums, tile, qf, vw, pg0.tile * kTile + 8 * g, live, a.sinks, a.c);
+                }
+                wait_loads<0>();
+                __syncthreads();
+            }
         } else {
             // Two tiles per wave in LDS, one on its way while the other is read (a
             // third did not help).  The loop over common tiles (every row sees every key, no
@@ -1011,22 +1082,20 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             // under way is always the same.
             bool wild = false;
             int c = c0 + wk;
-            uint32_t at = 0;                           // tile c's slot
-            auto tile_for = [&](int x) { return tile_at(min(x, c1 - 1)); };
-            auto pages_for = [&](int x) { return pages_of(a, trow, tile_for(x), sq.kv); };
-            Pages pg0{}, pg1{}, pg2{};                 // of tiles c, c + WK, c + 2 WK
+            uint32_t at = 0;                       // tile c's slot
+            Pages pg0{}, pg1{}, pg2{};             // of tiles c, c + WK, c + 2 WK
             if (c < c1) {
                 pg0 = pages_for(c);
                 pg1 = pages_for(c + WK);
                 pg2 = pages_for(c + 2 * WK);
-                fetch<FMT, D, 1, ONCE>(mine, a, pg0, tile_for(c), hk, lane, 0);
-                fetch<FMT, D, 1, ONCE>(mine + T::kBytes, a, pg1, tile_for(c + WK), hk, lane, 0);
+                fetch<FMT, D, ONCE>(mine, a, pg0, hk, lane);
+                fetch<FMT, D, ONCE>(mine + T::kBytes, a, pg1, hk, lane);
             }
             // the queries are used here, so that the wait for them is not left to
             // the loops below, where it would be for the tiles' loads too
-    #pragma unroll
+#pragma unroll
             for (int q = 0; q < MT; ++q)
-    #pragma unroll
+#pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     u32x4_t x = __builtin_bit_cast(u32x4_t, qf[q][s]);
                     asm volatile("" : "+v"(x));
@@ -1034,7 +1103,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 }
             // tile c is done with: its slot takes the next but one
             auto advance = [&] {
-                fetch<FMT, D, 1, ONCE>(mine + at, a, pg2, tile_for(c + 2 * WK), hk, lane, 0);
+                fetch<FMT, D, ONCE>(mine + at, a, pg2, hk, lane);
                 c += WK;
                 at ^= T::kBytes;
                 pg0 = pg1;
@@ -1043,7 +1112,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             };
             constexpr int kUnder = T::kFetches;
             while (c < c1) {
-                while (c < c1 && whole_at(tile_at(c) * kTile, pg0)) {
+                while (c < c1 && whole(pg0)) {
                     wait_loads<kUnder>();
                     if (!attend_whole<D, MT>(sums, RawTile<FMT, D>(base + at, lane), qf, a.c)) break;
                     advance();
@@ -1053,14 +1122,14 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 if (c >= c1) break;
                 // any tile
                 wait_loads<kUnder>();
-                const int key0 = tile_at(c) * kTile;
                 const RawTile<FMT, D> r(base + at, lane);
-                const uint32_t live = live_at(key0, pg0);
-                if (!whole_at(key0, pg0) && __any(r.wild(live))) wild = true;
-                else {
+                const uint32_t live = live_in(pg0);
+                if (!whole(pg0) && __any(r.wild(live))) {
+                    wild = true;
+                } else {
                     View vw[MT];
                     views(vw);
-                    attend_part<D, MT, false>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                    attend_part<D, MT, false>(sums, r, qf, vw, pg0.tile * kTile + 8 * g, live, a.sinks, a.c);
                 }
                 advance();
             }
@@ -1069,27 +1138,27 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             // that loop no registers.
             if (wild) {
                 for (c = c0 + wk; c < c1; c += WK) {
-                    const int key0 = tile_at(c) * kTile;
                     const Pages pc = pages_for(c);
-                    if (whole_at(key0, pc)) continue;
+                    if (whole(pc)) continue;
                     wait_loads<0>();
-                    fetch<FMT, D, 1, ONCE>(mine, a, pc, tile_at(c), hk, lane, 0);
+                    fetch<FMT, D, ONCE>(mine, a, pc, hk, lane);
                     wait_loads<0>();
                     const RawTile<FMT, D> r(base, lane);
-                    const uint32_t live = live_at(key0, pc);
+                    const uint32_t live = live_in(pc);
                     View vw[MT];
                     views(vw);
                     if (__any(r.wild(live)))
-                        attend_part<D, MT, true>(sums, r, qf, vw, key0 + 8 * g, live, a.sinks, a.c);
+                        attend_part<D, MT, true>(sums, r, qf, vw, pc.tile * kTile + 8 * g, live, a.sinks, a.c);
                 }
             }
-            wait_loads<0>();                           // the ring's memory is used again below
+            wait_loads<0>();                       // the ring's memory is used again below
         }
 
         // join the waves along the keys, 16 rows of each row wave at a time
 #pragma unroll
         for (int q = 0; q < MT; ++q) {
-            __syncthreads();
+            if (WK > 1 || q == 0) __syncthreads();
+            else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             if (g == 0) {
                 sh_m[wave][m] = sums.m[q];
                 sh_l[wave][m] = sums.l[q][0];
@@ -1106,7 +1175,8 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                         *reinterpret_cast<f32x4_t*>(row + (4 * g + i) * NT + n) =
                             f32x4_t{sums.o[q][n][i], sums.o[q][n + 1][i], sums.o[q][n + 2][i], sums.o[q][n + 3][i]};
             }
-            __syncthreads();
+            if constexpr (WK > 1) __syncthreads();
+            else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // a wave reads what it wrote
             const int wj = tid / TPR / 16, rr = tid / TPR % 16, d0 = tid % TPR * E;
             const int r = r0 + 16 * MT * wj + 16 * q + rr;
             if (r < rows) {
