@@ -254,24 +254,34 @@ __device__ __forceinline__ void fetch(uint32_t dst, const AttnArgs& a, const Pag
 }
 
 // The same where the workgroup's four waves share the tile: wave `part` starts
-// its loads, each of one half.
+// its loads, each of one half.  MXFP4: from these arrays, chosen once (chosen
+// anew, they would be read from the arguments for every tile).
+struct PartOf {
+    const uint8_t *data, *scale;
+    __device__ __forceinline__ PartOf(const AttnArgs& a, int part) {
+        data = part < 2 ? a.k : a.v;
+        scale = part < 2 ? a.ks : a.vs;
+        asm volatile("" : "+s"(data), "+s"(scale));
+    }
+};
 template <int FMT, int D>
-__device__ __forceinline__ void fetch_part(uint32_t dst, const AttnArgs& a, const Pages& pg, int hk, int lane, int part) {
+__device__ __forceinline__ void fetch_part(uint32_t dst, const AttnArgs& a, const PartOf& from, const Pages& pg, int hk, int lane,
+                                           int part) {
     using T = Tile<FMT, D>;
     if constexpr (FMT == MOE_KV_MXFP4) {
         const int h = part % 2;                    // keys or values of half h
         const bool keys = part < 2;
         const int64_t b = half_row(a, h ? pg.b : pg.a, pg.tile * kTile + 16 * h, hk);
-        const uint8_t* src = (keys ? a.k : a.v) + b * (D / 2);
+        const uint8_t* src = from.data + b * (D / 2);
         const uint32_t to = dst + (keys ? 0 : T::kValues) + h * (8 * D);
         if constexpr (D == 128) {
             const int chunk = keys ? (lane % 4) ^ (2 * h + lane / 32) : lane % 4;
             lds_dma16<false>(src, lane / 4 * 64 + chunk * 16, to);
-            lds_dma_low<16, 4>((keys ? a.ks : a.vs) + b * 4, lane * 4, dst + T::kScales + part * 64);
+            lds_dma_low<16, 4>(from.scale + b * 4, lane * 4, dst + T::kScales + part * 64);
         } else {
             const int chunk = keys ? (lane % 2) ^ ((lane / 16) & 1) : lane % 2;
             lds_dma_low<32, 16>(src, lane / 2 * 32 + chunk * 16, to);
-            lds_dma_low<8, 4>((keys ? a.ks : a.vs) + b * 2, lane * 4, dst + T::kScales + part * 32);
+            lds_dma_low<8, 4>(from.scale + b * 2, lane * 4, dst + T::kScales + part * 32);
         }
     } else {
         constexpr int C = D / 8, R = 64 / C, N = kTile / R / kWaves;    // chunks per row, rows per load, loads
@@ -422,7 +432,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0
 template <int D, int MT>
 struct Sums {
     f32x4_t o[MT][D / 16];                         // O^T
-    f32x4_t l[MT];                                 // the weights' sum, the same in all four
+    float l[MT];                                   // the weights' sum, of row lane % 16
     float m[MT];                                   // the reference, of row lane % 16
 };
 
@@ -487,7 +497,8 @@ __device__ __forceinline__ void weights(Sums<D, MT>& a, bf16x8_t (&pf)[MT], cons
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
         pf[q] = __builtin_bit_cast(bf16x8_t, w);
-        a.l[q] = mfma(ones, pf[q], a.l[q]);
+        // all four registers of the product are the same; one is kept
+        a.l[q] += mfma(ones, pf[q], f32x4_t{0.f, 0.f, 0.f, 0.f})[0];
     }
 }
 
@@ -951,7 +962,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
         for (int q = 0; q < MT; ++q) {
             // a lane without a row (queries of 0, scores of 0) never moves
             sums.m[q] = rw + 16 * q + m < rows ? -INFINITY : 0.f;
-            sums.l[q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            sums.l[q] = 0.f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) sums.o[q][n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
@@ -983,6 +994,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 const bool all = in_cache(a, p.a) && in_cache(a, p.b) && p.tile < sq.kv / kTile;
                 share_out<FMT, D>(raws + slot * T::kBytes, lds + slot * SharedTile<D>::kBytes, all ? 0u : live_in(p), all, wave, lane);
             };
+            const PartOf from(a, wave);
             int c = c0, buf = 0;                   // tile and its slot
             Pages pg0{}, pg1{}, pg2{};             // of tiles c, c + 1, c + 2
             auto begin = [&] {
@@ -992,8 +1004,8 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 pg0 = pages_for(c);
                 pg1 = pages_for(c + 1);
                 pg2 = pages_for(c + 2);
-                fetch_part<FMT, D>(raw_at, a, pg0, hk, lane, wave);
-                fetch_part<FMT, D>(raw_at + T::kBytes, a, pg1, hk, lane, wave);
+                fetch_part<FMT, D>(raw_at, a, from, pg0, hk, lane, wave);
+                fetch_part<FMT, D>(raw_at + T::kBytes, a, from, pg1, hk, lane, wave);
                 if constexpr (!DIRECT) {
                     wait_loads<0>();
                     lds_barrier();
@@ -1004,11 +1016,11 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
                 if constexpr (DIRECT) {
                     wait_loads<T::kFetches / kWaves>();        // tile c has arrived, this wave's part of it
                     lds_barrier();                 // and the others'; tile c - 1 is read
-                    fetch_part<FMT, D>(raw_at + (buf == 0 ? 2 : buf - 1) * T::kBytes, a, pg2, hk, lane, wave);
+                    fetch_part<FMT, D>(raw_at + (buf == 0 ? 2 : buf - 1) * T::kBytes, a, from, pg2, hk, lane, wave);
                 } else {
                     wait_loads<0>();               // tile c + 1 has arrived, this wave's part of it
                     lds_barrier();                 // and the others'; tile c is operands, c - 1 read
-                    fetch_part<FMT, D>(raw_at + buf * T::kBytes, a, pg2, hk, lane, wave);
+                    fetch_part<FMT, D>(raw_at + buf * T::kBytes, a, from, pg2, hk, lane, wave);
                     turn(buf ^ 1, pg1);
                 }
             };
@@ -1161,7 +1173,7 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
             else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             if (g == 0) {
                 sh_m[wave][m] = sums.m[q];
-                sh_l[wave][m] = sums.l[q][0];
+                sh_l[wave][m] = sums.l[q];
             }
             float* row = sh_o[wave][m];
             if constexpr (DIRECT) {
