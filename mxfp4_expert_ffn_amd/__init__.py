@@ -510,45 +510,25 @@ def _heads(t, D, device, name):
                      f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _int_tensors(device, *sizes):
-    """int32 tensors of these sizes on 16-byte boundaries, cut from one allocation."""
+def _handle_on(device, stream):
+    """The stream's handle where it and the device are current (``stream`` None: the device's current one), else
+    None: then the call has to be made again inside ``_made_current``."""
     import torch
-    cuts = [c for n in sizes for c in ((n, -n % 4) if n % 4 else (n,))]
-    parts = iter(torch.empty(sum(cuts), dtype=torch.int32, device=device).split_with_sizes(cuts))
-    out = []
-    for n in sizes:
-        out.append(next(parts))
-        if n % 4:
-            next(parts)
-    return out
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
+    if torch._C._cuda_getDevice() != device.index:
+        return None
+    # the current stream's handle as it is: a stream object for it costs as much as a launch
+    own = torch._C._cuda_getCurrentRawStream(device.index)
+    return own if stream is None or (stream.device == device and stream.cuda_stream == own) else None
 
 
-class _On:
-    """The device of a call's tensors and the stream it runs on, both current inside ``with``."""
-
-    __slots__ = ("_raw", "_ctx")
-
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {device}")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors on {device}")
-        # the current stream's handle: a stream object for it costs more than a launch
-        own = torch._C._cuda_getCurrentRawStream(device.index)
-        self._raw = own if stream is None else stream.cuda_stream
-        # the common case, all of it current already, enters nothing
-        self._ctx = (None if self._raw == own and torch.cuda.current_device() == device.index else
-                     torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream))
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self._raw
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _made_current(device, stream):
+    """The context in which the stream (None: the device's current one) and the device are current."""
+    import torch
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors on {device}")
+    return torch.cuda.stream(torch.cuda.current_stream(device) if stream is None else stream)
 
 
 class KvCache:
@@ -600,8 +580,9 @@ class KvCache:
         self.device = k.device
         self.struct = KvCacheStruct(ctypes.sizeof(KvCacheStruct), self.fmt, pages, ps, heads, D, k.data_ptr(), v.data_ptr(),
                                     k_scale.data_ptr() if fp4 else None, v_scale.data_ptr() if fp4 else None)
+        self.ref = ctypes.byref(self.struct)
         data, scale = ctypes.c_size_t(), ctypes.c_size_t()
-        _check(lib().moe_mxfp4_kv_cache_bytes(ctypes.byref(self.struct), ctypes.byref(data), ctypes.byref(scale)),
+        _check(lib().moe_mxfp4_kv_cache_bytes(self.ref, ctypes.byref(data), ctypes.byref(scale)),
                "moe_mxfp4_kv_cache_bytes")
 
 
@@ -621,29 +602,38 @@ def cache_plan(ctx_lens, new_lens, block_table, held, free_ring, free_state, *, 
     i32, dev = torch.int32, block_table.device
     B, W = block_table.shape
     N = free_ring.numel()
-    given = [(ctx_lens, (B,), "ctx_lens"), (new_lens, (B,), "new_lens"), (held, (B,), "held"),
-             (block_table, (B, W), "block_table"), (free_ring, (N,), "free_ring"), (free_state, (2,), "free_state")]
-    if held_out is not None:
-        given.append((held_out, (B,), "held_out"))
-    if free_out is not None:
-        given.append((free_out, (2,), "free_out"))
-    if out is not None:
-        given += [(out.cu_q, (B + 1,), "cu_q"), (out.kv_lens, (B,), "kv_lens"), (out.slots, (num_tokens,), "slots"),
-                  (out.positions, (num_tokens,), "positions"), (out.refused, (1,), "refused"),
-                  (out.held, (B,), "held_out"), (out.free_state, (2,), "free_out")]
-    for t, shape, name in given:
+    for t, shape, name in ((ctx_lens, (B,), "ctx_lens"), (new_lens, (B,), "new_lens"), (held, (B,), "held"),
+                           (block_table, (B, W), "block_table"), (free_ring, (N,), "free_ring"),
+                           (free_state, (2,), "free_state")):
         _like(t, i32, shape, dev, name)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = CachePlan(*_int_tensors(dev, B + 1, B, num_tokens, num_tokens, 1, B, 2))
-        if held_out is not None or free_out is not None:
-            out = out._replace(**{n: t for n, t in (("held", held_out), ("free_state", free_out)) if t is not None})
-        args = PlanArgs(ctypes.sizeof(PlanArgs), B, num_tokens, W, page_size, N, ctx_lens.data_ptr(), new_lens.data_ptr(),
-                        block_table.data_ptr(), held.data_ptr(), out.held.data_ptr(), free_ring.data_ptr(),
-                        free_state.data_ptr(), out.free_state.data_ptr(), out.cu_q.data_ptr(), out.kv_lens.data_ptr(),
-                        out.slots.data_ptr(), out.positions.data_ptr(), out.refused.data_ptr())
-        _check(lib().moe_mxfp4_cache_plan(ctypes.byref(args), st), "moe_mxfp4_cache_plan")
-    return out
+    st = _handle_on(dev, stream)
+    if st is None:
+        with _made_current(dev, stream):
+            return cache_plan(ctx_lens, new_lens, block_table, held, free_ring, free_state, page_size=page_size,
+                              num_tokens=num_tokens, held_out=held_out, free_out=free_out, out=out)
+    if out is None:
+        # one allocation, cut up on 16-byte boundaries
+        T, pb = num_tokens, -(B + 1) % 4
+        parts = torch.empty(2 * (B + T) + 20, dtype=i32, device=dev).split_with_sizes(
+            (1, 3, B + 1, pb, B, -B % 4, T, -T % 4, T, 15 - pb - -B % 4 - -T % 4))
+        cu_q, kv_lens, slots, positions, refused = parts[2], parts[4], parts[6], parts[8], parts[0]
+        held_out = torch.empty(B, dtype=i32, device=dev) if held_out is None else held_out
+        free_out = torch.empty(2, dtype=i32, device=dev) if free_out is None else free_out
+    else:
+        cu_q, kv_lens, slots, positions, refused = out[:5]
+        held_out = out.held if held_out is None else held_out
+        free_out = out.free_state if free_out is None else free_out
+        for t, n, name in ((cu_q, B + 1, "cu_q"), (kv_lens, B, "kv_lens"), (slots, num_tokens, "slots"),
+                           (positions, num_tokens, "positions"), (refused, 1, "refused")):
+            _like(t, i32, (n,), dev, name)
+    _like(held_out, i32, (B,), dev, "held_out")
+    _like(free_out, i32, (2,), dev, "free_out")
+    args = PlanArgs(ctypes.sizeof(PlanArgs), B, num_tokens, W, page_size, N, ctx_lens.data_ptr(), new_lens.data_ptr(),
+                    block_table.data_ptr(), held.data_ptr(), held_out.data_ptr(), free_ring.data_ptr(),
+                    free_state.data_ptr(), free_out.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(),
+                    positions.data_ptr(), refused.data_ptr())
+    _check(lib().moe_mxfp4_cache_plan(ctypes.byref(args), st), "moe_mxfp4_cache_plan")
+    return CachePlan(cu_q, kv_lens, slots, positions, refused, held_out, free_out)
 
 
 def qk_norm_rope(q, k, v, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -661,7 +651,7 @@ def qk_norm_rope(q, k, v, positions, inv_freq, *, q_weight=None, k_weight=None, 
     T, H, D = q.shape
     HK = k.shape[1]
     qs, ks = _heads(q, D, dev, "q"), _heads(k, D, dev, "k")
-    vs = 0
+    vs, v_ptr, slots_ptr, cache_ref = 0, None, None, None
     if k.shape[0] != T:
         raise ValueError(f"k: {k.shape[0]} tokens, q has {T}")
     _like(positions, torch.int32, (T,), dev, "positions")
@@ -676,23 +666,25 @@ def qk_norm_rope(q, k, v, positions, inv_freq, *, q_weight=None, k_weight=None, 
         _like(slots, torch.int32, (T,), dev, "slots")
         if cache.device != dev:
             raise ValueError(f"cache on {cache.device}, q on {dev}")
-    with _On(dev, stream) as st:
-        if q_out is None:
-            q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
-        else:
-            _like(q_out, torch.bfloat16, (T, H, D), dev, "q_out")
-        if k_out is not None:
-            _like(k_out, torch.bfloat16, (T, HK, D), dev, "k_out")
-        elif cache is None:
-            k_out = torch.empty((T, HK, D), dtype=torch.bfloat16, device=dev)
-        args = RopeArgs(ctypes.sizeof(RopeArgs), T, H, HK, D, 2 * inv_freq.numel(), int(interleaved), eps, qs, ks, vs,
-                        q.data_ptr(), k.data_ptr(), None if cache is None else v.data_ptr(),
-                        None if q_weight is None else q_weight.data_ptr(),
-                        None if k_weight is None else k_weight.data_ptr(), inv_freq.data_ptr(), positions.data_ptr(),
-                        None if cache is None else slots.data_ptr(), q_out.data_ptr(),
-                        None if k_out is None else k_out.data_ptr())
-        _check(lib().moe_mxfp4_qk_norm_rope(ctypes.byref(args), None if cache is None else ctypes.byref(cache.struct),
-                                            st), "moe_mxfp4_qk_norm_rope")
+        v_ptr, slots_ptr, cache_ref = v.data_ptr(), slots.data_ptr(), cache.ref
+    st = _handle_on(dev, stream)
+    if st is None:
+        with _made_current(dev, stream):
+            return qk_norm_rope(q, k, v, positions, inv_freq, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                                interleaved=interleaved, cache=cache, slots=slots, q_out=q_out, k_out=k_out)
+    if q_out is None:
+        q_out = q.new_empty((T, H, D))
+    else:
+        _like(q_out, torch.bfloat16, (T, H, D), dev, "q_out")
+    if k_out is not None:
+        _like(k_out, torch.bfloat16, (T, HK, D), dev, "k_out")
+    elif cache is None:
+        k_out = q.new_empty((T, HK, D))
+    args = RopeArgs(ctypes.sizeof(RopeArgs), T, H, HK, D, 2 * inv_freq.numel(), int(interleaved), eps, qs, ks, vs,
+                    q.data_ptr(), k.data_ptr(), v_ptr, None if q_weight is None else q_weight.data_ptr(),
+                    None if k_weight is None else k_weight.data_ptr(), inv_freq.data_ptr(), positions.data_ptr(),
+                    slots_ptr, q_out.data_ptr(), None if k_out is None else k_out.data_ptr())
+    _check(lib().moe_mxfp4_qk_norm_rope(ctypes.byref(args), cache_ref, st), "moe_mxfp4_qk_norm_rope")
     return q_out, k_out
 
 
@@ -701,10 +693,12 @@ def kv_read(cache: KvCache, slots, stream=None):
     import torch
     n, dev = slots.numel(), cache.device
     _like(slots, torch.int32, (n,), dev, "slots")
-    with _On(dev, stream) as st:
-        k, v = torch.empty((2, n, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=dev).unbind()
-        _check(lib().moe_mxfp4_kv_read(ctypes.byref(cache.struct), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
-                                       st), "moe_mxfp4_kv_read")
+    st = _handle_on(dev, stream)
+    if st is None:
+        with _made_current(dev, stream):
+            return kv_read(cache, slots)
+    k, v = torch.empty((2, n, cache.kv_heads, cache.head_dim), dtype=torch.bfloat16, device=dev).unbind()
+    _check(lib().moe_mxfp4_kv_read(cache.ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), st), "moe_mxfp4_kv_read")
     return k, v
 
 
@@ -729,25 +723,33 @@ def attention(q, cache: KvCache, block_table, cu_q, kv_lens, *, max_q: int, max_
     _like(kv_lens, torch.int32, (B,), dev, "kv_lens")
     if cache.head_dim != D or cache.device != dev:
         raise ValueError(f"q has heads of {D} on {dev}, the cache of {cache.head_dim} on {cache.device}")
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
-        elif out.shape != q.shape:
+    st = _handle_on(dev, stream)
+    if st is None:
+        with _made_current(dev, stream):
+            return attention(q, cache, block_table, cu_q, kv_lens, max_q=max_q, max_kv=max_kv, scale=scale, causal=causal,
+                             window=window, sinks=sinks, out=out, workspace=workspace)
+    if out is None:
+        out, os_ = q.new_empty((T, H, D)), H * D
+    else:
+        if out.shape != q.shape:
             raise ValueError(f"out: expected {tuple(q.shape)}, got {tuple(out.shape)}")
-        args = AttnArgs(ctypes.sizeof(AttnArgs), B, T, H, max_q, max_kv, W, int(causal), window, sinks,
-                        D ** -0.5 if scale is None else scale, qs, _heads(out, D, dev, "out"), q.data_ptr(),
-                        out.data_ptr(), block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr())
-        L, a, c = lib(), ctypes.byref(args), ctypes.byref(cache.struct)
-        if workspace is None:
-            need = L.moe_mxfp4_attention_workspace_bytes(a, c)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif workspace.device != dev:
-            raise ValueError(f"workspace on {workspace.device}, q on {dev}")
-        if workspace is None:
-            status = L.moe_mxfp4_attention(a, c, None, 0, st)
-        else:
-            status = L.moe_mxfp4_attention(a, c, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st)
-        _check(status, "moe_mxfp4_attention")
+        os_ = _heads(out, D, dev, "out")
+    args = ctypes.byref(AttnArgs(ctypes.sizeof(AttnArgs), B, T, H, max_q, max_kv, W, int(causal), window, sinks,
+                                 D ** -0.5 if scale is None else scale, qs, os_, q.data_ptr(), out.data_ptr(),
+                                 block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr()))
+    L = lib()
+    if workspace is None:
+        need = L.moe_mxfp4_attention_workspace_bytes(args, cache.ref)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace on {workspace.device}, q on {dev}")
+    if workspace is None:
+        status = L.moe_mxfp4_attention(args, cache.ref, None, 0, st)
+    else:
+        status = L.moe_mxfp4_attention(args, cache.ref, workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), st)
+    _check(status, "moe_mxfp4_attention")
     return out
 
 
