@@ -389,6 +389,10 @@ __device__ __forceinline__ void v_operand(const Raw<FMT, D>& r, uint32_t live, b
     second = __builtin_bit_cast(bf16x8_t, hi);
 }
 
+// Two bf16 at once: a bit of 0x80008000 is set where one's exponent, kept by
+// mask (0x7F80 of it), is all ones.
+__device__ __forceinline__ uint32_t wild2(uint32_t w, uint32_t mask) { return (w & mask) + 0x00800080u; }
+
 // Whether a live key of this lane has an infinite or NaN value (MXFP4: a
 // scale with which 6 passes float32's range, or NaN).
 template <int FMT, int D>
@@ -396,17 +400,15 @@ __device__ __forceinline__ bool wild_values(const Raw<FMT, D>& r, uint32_t live)
     uint32_t wild = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        bool x = false;
+        const bool on = (live >> j) & 1;
         if constexpr (FMT == MOE_KV_MXFP4) {
-            x = ((r.vb[j / 4] >> (8 * (j % 4))) & 0xFF) >= 253;
+            wild |= on && ((r.vb[j / 4] >> (8 * (j % 4))) & 0xFF) >= 253 ? 0x8000u : 0u;
         } else {
 #pragma unroll
-            for (int u = 0; u < D / 32; ++u)
-                x |= (r.v[j][u] & 0x7F80u) == 0x7F80u || (r.v[j][u] & 0x7F800000u) == 0x7F800000u;
+            for (int u = 0; u < D / 32; ++u) wild |= wild2(r.v[j][u], on ? 0x7F807F80u : 0u);
         }
-        wild |= (uint32_t)x << j;
     }
-    return (wild & live) != 0;
+    return (wild & 0x80008000u) != 0;
 }
 
 __device__ __forceinline__ f32x4_t mfma(const bf16x8_t& x, const bf16x8_t& y, const f32x4_t& c) {
@@ -571,15 +573,17 @@ template <int D, typename Tile_> struct Masked : Tile_ {
     }
     // whether one of the lane group's live keys has an infinite or NaN value
     __device__ __forceinline__ bool wild(uint32_t live) const {
-        bool x = false;
+        uint32_t mask[4], x = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mask[i] = ((live >> (2 * i)) & 1 ? 0x7F80u : 0u) | ((live >> (2 * i + 1)) & 1 ? 0x7F800000u : 0u);
+#pragma unroll
         for (int n = 0; n < D / 16; ++n) {
             const u32x4_t w = __builtin_bit_cast(u32x4_t, this->value(n));
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x |= ((live >> (2 * i)) & 1 && (w[i] & 0x7F80u) == 0x7F80u) ||
-                     ((live >> (2 * i + 1)) & 1 && (w[i] & 0x7F800000u) == 0x7F800000u);
+            for (int i = 0; i < 4; ++i) x |= wild2(w[i], mask[i]);
         }
-        return x;
+        return (x & 0x80008000u) != 0;
     }
     __device__ __forceinline__ void anew() {}
 };
@@ -941,13 +945,16 @@ __global__ __launch_bounds__(kThreads, WPE) void k_attn(AttnArgs a) {
         }
         // what they see; found anew for each tile that needs it, since kept it
         // would cost the common tiles registers
+        const int tok0 = rw / a.G, in0 = rw % a.G;
+        const float per_token = 1.0f / (float)a.G;
         auto views = [&](View (&vw)[MT]) {
-            int first = rw + m;
+            int first = m;
             asm volatile("" : "+v"(first));
 #pragma unroll
             for (int q = 0; q < MT; ++q) {
-                const int r = first + 16 * q, p = sq.kv - sq.n + (int)((unsigned)r / (unsigned)a.G);
-                vw[q].up = r >= rows || p < 0 ? 0 : a.causal ? min(p + 1, sq.kv) : sq.kv;
+                // (x + 1/2) / G is at least 1 / 2G from a whole number, and x below 2^15
+                const int x = first + 16 * q, t = (int)(((float)(in0 + x) + 0.5f) * per_token), p = sq.kv - sq.n + tok0 + t;
+                vw[q].up = rw + x >= rows || p < 0 ? 0 : a.causal ? min(p + 1, sq.kv) : sq.kv;
                 vw[q].lo = a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
             }
         };
