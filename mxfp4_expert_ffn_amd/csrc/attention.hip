@@ -16,18 +16,31 @@
 // bytes of an MXFP4 key row of 128 and one MX block.  V^T's row m of the
 // product's tile tau is element m D/16 + tau, so a lane needs D/16 consecutive elements of
 // its 8 keys, decodes pairs of elements with their key's scale and regroups
-// halves of registers by key.  Both operands come straight from memory into
-// registers; V's codes are stored so that these are 16-byte loads.
+// halves of registers by key; V's codes are stored so that these are 16-byte
+// reads.
 //
 // Decoding E2M1 x E8M0 to bf16 is exact, queries are bf16 as given, scores and
 // statistics float32; the softmax weights are rounded to bf16 for the second
-// product (a relative 2^-9 each, as the operand type asks).  The row maximum
-// is only a reference point: it is moved when some score of the tile passes it
-// by 2^8, so most tiles need neither a lane exchange nor a rescaling.
+// product (a relative 2^-9 each, as the operand type asks), and their sum is
+// taken from the rounded ones.  The row maximum is only a reference point: it
+// is moved when some score of the tile passes it by 2^8, so most tiles need
+// neither a lane exchange nor a rescaling.
 //
-// Four waves of a workgroup take every fourth tile of the workgroup's share
-// of the keys and join their sums through LDS.  Where there are few (sequence,
-// head) pairs the keys are shared by several workgroups, which leave float32
+// Tiles go from memory to LDS without registers, a tile or two ahead of their
+// use.  Up to 64 rows: four waves take every fourth tile of the workgroup's
+// keys, each through a ring of its own, read it as stored and decode it in
+// registers, and their sums are joined through LDS.  Those kernels are bound
+// by the cache's bytes (64 sequences, one token each, 0.7 GB of MXFP4: 146-149
+// us, 4.8-4.9 TB/s; a window of 1000 in bf16, 0.14 GB: 30 us, 4.7 TB/s) and,
+// with more rows a key, by decoding (32 sequences, 8 tokens each: 57-61 us; the
+// decode of a tile is 64 converts and 32 permutes whatever the rows).  More
+// rows: the four waves take 48 rows each (64 of D = 64) and share every tile,
+// decoded once into operands in LDS, so that its cost is divided by 192 rows.
+// Those are bound by the matrix cores and by the LDS reads that feed them
+// (2048 tokens behind 6144, 48 heads: 353 us a call, 1.02 PFLOP/s).
+//
+// Where there are few (sequence, head, set of rows) the keys of all of them
+// are divided evenly over the workgroups the GPU holds, which leave float32
 // sums that k_attn_join adds up in order.
 #include <type_traits>
 
@@ -1322,7 +1335,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a, int per, int
 // Launch shape: a function of the sizes alone, so that the workspace's size
 // and the launch agree.
 // 16-row tiles of a wave where four waves along the rows share each tile of
-// keys: what 256 registers hold.
+// keys: what 256 registers hold.  Two, with three workgroups a CU: 443 against
+// 424 us (MXFP4 chunk) and 228 against 201 us (bf16 windowed prompts).
 constexpr int shared_mt(int D) { return D == 128 ? 3 : 4; }
 struct Shape {
     int mode, mt, wr, row_tiles, grid;
@@ -1350,10 +1364,11 @@ Shape shape_of(const moe_mxfp4_attn_args& p, const moe_mxfp4_kv_cache& c) {
         if (w < keys) keys = w;
     }
     const int64_t pairs = (int64_t)p.batch * c.kv_heads;
-    // Quotas where sequences are long enough to be divided and few sets of
-    // rows share their keys; not where a window makes them all alike and
-    // there are enough of them (64 sequences x 8 heads of a window of 1000:
-    // 37 us, and 38 us + 18 us for the join with quotas).
+    // Quotas where sequences are long enough to be divided and too few sets of
+    // rows to fill the GPU, of which ragged ones would leave it early (a
+    // 2048-token chunk, 512 sets: 446 us without, 474 + 32 for the join with
+    // quotas); not where a window makes them all alike and there are enough of
+    // them (64 sequences x 8 heads of a window of 1000: 30 us, 38 + 18 with).
     const int64_t held = 256 * (wide && s.wr < kWaves ? 1 : s.mt == 1 && fp4 ? 3 : 2);   // workgroups the GPU holds at once
     const bool alike = p.window > 0 && keys < p.max_kv && pairs * tiles >= held;
     if (p.batch <= kQuotaBatch && pairs * tiles < held && (keys + kTile - 1) / kTile > kQuotaLeast && !alike) {

@@ -13,9 +13,11 @@
 // R/2 angles of a token are computed once per workgroup, one a thread, into
 // LDS.
 //
-// Bound by bytes (2 (2 Hq + 2 Hkv) D a token and the cache row).  Few tokens:
-// a token's heads are split over up to four workgroups, so that every wave
-// has one load round instead of four in sequence.
+// Bound by bytes (2 (2 Hq + 2 Hkv) D a token and the cache row): 5570
+// tokens of 48 + 8 + 8 heads of 128, 165 MB, 40 us, 4.1 TB/s.  Few tokens: bound by the launch and one chain of
+// loads (8 tokens 4.2 us, 512 tokens 6.8 us); a token's heads are split over
+// up to four workgroups, so that every wave has one load round instead of four
+// in sequence.
 #include "kv_cache.hpp"
 
 namespace moe {
