@@ -742,8 +742,9 @@ def attention(q, cache: KvCache, block_table, cu_q, kv_lens, *, max_q: int, max_
         need = L.moe_mxfp4_attention_workspace_bytes(args, cache.ref)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace on {workspace.device}, q on {dev}")
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {dev}, got strides {workspace.stride()} on "
+                         f"{workspace.device}")
     if workspace is None:
         status = L.moe_mxfp4_attention(args, cache.ref, None, 0, st)
     else:

@@ -164,3 +164,22 @@ def test_two_graphs_of_two_workspaces_and_eager_calls_between():
         torch.cuda.synchronize()
         for r, e in zip(runs, eager):
             assert torch.equal(r["out"], r["want"]) and torch.equal(e, r["want"]), turn
+
+
+def test_workspace_that_is_not_one_piece_is_refused():
+    """Bytes counted through strides need not be there."""
+    moe = _moe()
+    rng = np.random.default_rng(7700)
+    p = problem(rng, True, 64, 1, 2, 16, [2], [900])
+    cache, q = to_device(moe, p["hc"]), bf16(p["q"])
+    args = (q, cache, dev(p["table"]), dev(p["cu"]), dev(p["lens"]))
+    need = moe.attention_workspace_bytes(cache, 2, 2, 1, max_q=2, max_kv=900)
+    assert need > 0
+    whole = torch.empty(2 * need, dtype=torch.uint8, device="cuda")
+    for ws in (whole[:16].view(1, 16).expand(need, 16), whole[::2], whole[:need].cpu()):
+        with pytest.raises(ValueError, match="workspace"):
+            moe.attention(*args, max_q=2, max_kv=900, workspace=ws)
+    with pytest.raises(moe.MoeError):
+        moe.attention(*args, max_q=2, max_kv=900, workspace=whole[1:])          # not on a 16-byte boundary
+    want, _, _ = check(moe, p, cache=cache)
+    assert torch.equal(moe.attention(*args, max_q=2, max_kv=900, workspace=whole), want)
